@@ -10,6 +10,11 @@
  *   fm_moe_gather_gemm   token gather fused with grouped expert GEMM (MoE layer 0)
  *   fm_moe_gemm_scatter  grouped expert GEMM fused with top-k weighted
  *                        scatter-reduce (MoE layer 1)
+ * and what stands around them in a sparse block: the router with its balance
+ * loss (fm_moe_gate, fm_moe_gate_bwd), the norms, gate and residual add between
+ * two blocks (fm_norm_residual, fm_norm_residual_bwd), and the products of a
+ * decode step with 4-bit weights (fm_gemm_w4, fm_moe_gather_gemm_w4,
+ * fm_moe_gemm_scatter_w4),
  * plus the AllGather variants fm_ag_gemm_pull (chunks read in place),
  * fm_ag_gemm_producers (copies done by workgroups of the same launch),
  * fm_moe_ag_gather_gemm (MoE layer 0 behind a token AllGather) with its
@@ -500,6 +505,202 @@ fm_status_t fm_moe_gemm_scatter_noalloc(fm_dtype_t dt, int64_t T, int64_t hidden
                                         const float* topk_weights, float* out,
                                         int32_t* err_word, int64_t spin_limit,
                                         hipStream_t stream);
+
+/*
+ * fm_moe_gate -- router of an MoE layer: the experts and weights of each token
+ * from its router logits, and the layer's expert counts and balance loss.
+ * With x = logits[t, :] in fp32 and
+ *   u = x           (FM_GATE_SOFTMAX)      share = softmax(u) over all experts
+ *   u = log s(x)    (FM_GATE_SIGMOID)      s(x) = 1 / (1 + exp(-x))
+ * the score of an expert is share (softmax) or s(x) (sigmoid), and
+ *   topk_ids[t, :]      the topk experts with the largest key, largest first,
+ *                       equal keys by the lower expert.  The key is x, or with
+ *                       a bias score + bias, evaluated in 64 bits.
+ *   topk_weights[t, :]  scale * score of these experts or, renormalized,
+ *                       scale * softmax of u over the chosen ones.
+ *   counts[e]           slots of topk_ids that name expert e; counts[E] the
+ *                       number of tokens that are not masked, n.
+ *   prob_sums[e]        sum of share[t, e] over the tokens not masked.
+ *   loss                E / (topk n^2) * sum_e counts[e] * prob_sums[e]; 1 for
+ *                       perfectly even experts, 0 if n = 0.
+ * topk_ids and topk_weights are what fm_moe_route and fm_moe_gemm_scatter take.
+ *   dt, logits  FM_F16, FM_BF16 or FM_F32, [T, n_experts]; n_experts 1..1024.
+ *               An expert with logit -inf is closed: it is never chosen, and
+ *               its share is 0.  A slot that finds no open expert gets id -1
+ *               and weight 0, which every MoE call here passes over.  A NaN
+ *               is never chosen; it (or +inf under a softmax) makes its row's
+ *               shares, and so prob_sums and the loss, NaN.
+ *   topk        1..16 and <= n_experts.
+ *   bias        fp32 [n_experts] or NULL; it only moves the choice.
+ *   token_mask  uint8 [T] or NULL: tokens with 0 are padding.  Their logits are
+ *               not used, their ids are -1 and their weights 0.
+ *   counts      int32 [n_experts + 1], prob_sums fp32 [n_experts], loss fp32
+ *               [1]: all three written, or all three NULL (then no workspace
+ *               is needed).
+ *   ws, ws_bytes  scratch of fm_moe_gate_workspace_bytes, 16-byte aligned; its
+ *               contents need no preparation.  Calls that may run at the same
+ *               time, captured graphs' replays among them, need one each.
+ * Deterministic: identical bits on every call.
+ */
+typedef enum fm_gate_score { FM_GATE_SOFTMAX = 0, FM_GATE_SIGMOID = 1 } fm_gate_score_t;
+
+size_t fm_moe_gate_workspace_bytes(int64_t T, int32_t n_experts);
+
+fm_status_t fm_moe_gate(fm_dtype_t dt, int64_t T, int32_t n_experts, int32_t topk,
+                        fm_gate_score_t score, int32_t renormalize, float scale,
+                        const void* logits, const float* bias, const uint8_t* token_mask,
+                        int32_t* topk_ids, float* topk_weights, int32_t* counts,
+                        float* prob_sums, float* loss, void* ws, size_t ws_bytes,
+                        hipStream_t stream);
+
+/*
+ * fm_moe_gate_bwd -- gradient of fm_moe_gate's weights and loss: d_logits from
+ * d_weights (gradient of topk_weights) and d_loss (gradient of the loss).  The
+ * choice of experts, the counts and the bias carry no gradient.
+ *   topk_ids   as fm_moe_gate left them: slots outside [0, n_experts) take no
+ *              part; a repeated expert adds up.
+ *   d_weights  fp32 [T, topk], or NULL: no gradient by that way.
+ *   counts     int32 [n_experts + 1] and d_loss, a device fp32, or both NULL.
+ *              With counts (and n) summed over data-parallel ranks this is the
+ *              gradient of the loss of the whole batch.
+ *   d_logits   [T, n_experts] in dt (written whole: 0 for masked tokens and
+ *              closed experts).  It must not overlap logits.
+ *   the rest   as fm_moe_gate.
+ */
+fm_status_t fm_moe_gate_bwd(fm_dtype_t dt, int64_t T, int32_t n_experts, int32_t topk,
+                            fm_gate_score_t score, int32_t renormalize, float scale,
+                            const void* logits, const uint8_t* token_mask,
+                            const int32_t* topk_ids, const float* d_weights,
+                            const int32_t* counts, const float* d_loss, void* d_logits,
+                            hipStream_t stream);
+
+/*
+ * fm_norm_residual -- what lies between two blocks of a residual stream: the
+ * norm after a block, its gate and scale, the residual add and the norm before
+ * the next block, in one pass.  For each row
+ *   b   = block                               or, with w_post,
+ *         block / rms(block) * w_post         rms(v) = sqrt(mean(v^2) + eps)
+ *   out = resid + scale * gate * b
+ *   y   = out / rms(out) * w_pre
+ * all in fp32 (y from the fp32 value of out), rounded once when stored.  block
+ * may be a slice that fm_gemm_rs filled or the combine's out (fp32); y is the
+ * 16-bit input of fm_ag_gemm, fm_chunk_push or fm_moe_gather_gemm.
+ *   dt         FM_F16 or FM_BF16: y, w_post, w_pre and gate.
+ *   stream_dt  resid and out: dt or FM_F32.   block_dt  block: dt or FM_F32.
+ *   M, N       rows and row length; N a multiple of 8, at most 16384.
+ *   block      [M, N] or NULL: no block (out = resid; w_post and gate must be
+ *              NULL too).   resid  [M, N] or NULL: 0.  Not both NULL.
+ *   w_post, w_pre  [N] or NULL: no norm there.  y is NULL if and only if w_pre is.
+ *   gate       [n_gates, N] or NULL: 1.  Row i takes gate row i / (M / n_gates);
+ *              M is a multiple of n_gates (1: one for all, M: one per row,
+ *              else one for each sequence of M / n_gates rows).
+ *   out        [M, N] or NULL (not wanted); it may be resid itself.
+ *   rstd_post, rstd_pre  fp32 [M] or NULL: 1 / rms, which the backward needs.
+ */
+fm_status_t fm_norm_residual(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t block_dt, int64_t M,
+                             int64_t N, const void* block, const void* resid, const void* w_post,
+                             const void* w_pre, const void* gate, int64_t n_gates, float scale,
+                             float eps, void* out, void* y, float* rstd_post, float* rstd_pre,
+                             hipStream_t stream);
+
+/*
+ * fm_norm_residual_bwd -- gradients of fm_norm_residual.
+ *   d_y      [M, N] dt, gradient of y; NULL if and only if w_pre is.
+ *   d_out    [M, N] stream_dt, gradient of out from its later uses, or NULL: 0.
+ *   out      [M, N] stream_dt as the forward stored it; needed with w_pre.
+ *   block    [M, N] block_dt; needed with w_post or d_gate.
+ *   rstd_post, rstd_pre  as the forward stored them; needed with w_post, w_pre.
+ *   d_resid  [M, N] stream_dt or NULL: gradient of resid (of out in total).
+ *            It may be d_out itself.
+ *   d_block  [M, N] block_dt or NULL.
+ *   d_w_post, d_w_pre fp32 [N], d_gate fp32 [n_gates, N]: written whole, or
+ *            NULL; each only beside its weight.
+ *   ws, ws_bytes  scratch of fm_norm_residual_workspace_bytes, 16-byte aligned,
+ *            without preparation; needed if any of these three is wanted, one
+ *            for each call that may run at the same time.
+ * The column sums are taken in a fixed order: identical bits on every call.
+ */
+size_t fm_norm_residual_workspace_bytes(int64_t M, int64_t N, int64_t n_gates);
+
+fm_status_t fm_norm_residual_bwd(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t block_dt,
+                                 int64_t M, int64_t N, const void* d_y, const void* d_out,
+                                 const void* out, const void* block, const void* w_post,
+                                 const void* w_pre, const void* gate, int64_t n_gates,
+                                 float scale, const float* rstd_post, const float* rstd_pre,
+                                 void* d_resid, void* d_block, float* d_w_post, float* d_w_pre,
+                                 float* d_gate, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * 4-bit weights.  A [K, N] matrix is N * fm_w4_row_bytes(K) packed bytes, with
+ *   W[k, n] = (code[k, n] - zero[k / group, n]) * scale[k / group, n],
+ * codes 0..15; scales [ceil(K / group), N] in the activations' type; zeros
+ * uint8 of the same shape, or NULL: 8 everywhere; group 32, 64 or 128 (the last
+ * group of a K may be short).  Column n is a row of fm_w4_row_bytes(K) =
+ * 64 * ceil(K / 128) bytes.  Each 64-byte block holds 128 k as 16 little-endian
+ * words: word 4 q + j holds k = 32 j + 8 q + 0..7, its nibble p, from the low
+ * end, the k offset 2 p for p < 4 and 2 (p - 4) + 1 for p >= 4 (so that one
+ * 16-byte load of a lane feeds four matrix instructions).  Codes past K are
+ * not used.
+ *
+ * fm_w4_pack -- packed bytes from codes, uint8 [n_matrices, K, N], values
+ * 0..15 (the high four bits are dropped).  Done once when weights are loaded.
+ */
+size_t fm_w4_row_bytes(int64_t K);
+
+fm_status_t fm_w4_pack(int64_t n_matrices, int64_t K, int64_t N, const uint8_t* codes,
+                       void* packed, hipStream_t stream);
+
+/*
+ * fm_gemm_w4 -- fm_gemm with a 4-bit B, for few rows (a decode step):
+ * C[M, N] = A[M, K] * W[K, N].  The weights are read once for every 32 rows;
+ * for hundreds of rows, unpacked 16-bit weights and fm_gemm are faster.
+ *   ab      FM_F16 or FM_BF16: A and scales;  c  ab or FM_F32.
+ *   packed  as above, 16-byte aligned; scales 16-byte aligned.
+ * Codes enter the matrix cores exactly; products are summed in fp32 group by
+ * group and scaled there.  A must be finite: an infinite or NaN A[m, k] makes
+ * row m of C NaN or infinite.
+ */
+fm_status_t fm_gemm_w4(fm_dtype_t ab, fm_dtype_t c, int64_t M, int64_t N, int64_t K,
+                       int32_t group, const void* A, const void* packed, const void* scales,
+                       const uint8_t* zeros, void* C, hipStream_t stream);
+
+/*
+ * fm_moe_gather_gemm_w4 -- fm_moe_gather_gemm_act with 4-bit weights, for the
+ * few tokens of a decode step: packed, scales and zeros hold n_local
+ * [hidden, ffn] matrices.  The other arguments, sorted_pairs, expert_offsets
+ * and the rows of H behind them as there; ws is that call's workspace.
+ * Experts without a token are not read.
+ */
+fm_status_t fm_moe_gather_gemm_w4(fm_dtype_t dt, int64_t T, int64_t hidden, int64_t ffn,
+                                  int32_t topk, int32_t expert_begin, int32_t n_local,
+                                  int32_t group, const void* X, const int32_t* topk_ids,
+                                  const void* packed, const void* scales, const uint8_t* zeros,
+                                  void* H, int32_t* sorted_pairs, int32_t* expert_offsets,
+                                  fm_act_t act, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * fm_moe_gemm_scatter_w4 -- the combine with 4-bit weights, for few tokens:
+ *   out[t, :] = add[t, :] + sum over local pairs p = t*topk + k of
+ *               topk_weights[p] * (H[row(p), :] * W2[e(p)])
+ * summed in the order of k.  packed, scales and zeros hold n_local
+ * [ffn, hidden] matrices; H, sorted_pairs and expert_offsets are those of
+ * fm_moe_gather_gemm_w4 (or fm_moe_gather_gemm) with the same topk_ids and
+ * expert_begin.  Two pairs of a token may name one expert.
+ *   add  fp32 [T, hidden] or NULL: 0; it may be out itself (out += ...).
+ *   ws, ws_bytes  scratch of fm_moe_w4_workspace_bytes, 16-byte aligned,
+ *        without preparation; one for each call that may run at the same time.
+ * Deterministic: identical bits on every call.
+ */
+size_t fm_moe_w4_workspace_bytes(int64_t T, int32_t topk, int64_t hidden);
+
+fm_status_t fm_moe_gemm_scatter_w4(fm_dtype_t dt, int64_t T, int64_t hidden, int64_t ffn,
+                                   int32_t topk, int32_t expert_begin, int32_t n_local,
+                                   int32_t group, const void* H, const void* packed,
+                                   const void* scales, const uint8_t* zeros,
+                                   const int32_t* topk_ids, const int32_t* sorted_pairs,
+                                   const int32_t* expert_offsets, const float* topk_weights,
+                                   const float* add, float* out, void* ws, size_t ws_bytes,
+                                   hipStream_t stream);
 
 #ifdef __cplusplus
 }

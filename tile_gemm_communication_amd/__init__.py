@@ -26,10 +26,16 @@ EXPORTS = ("fm_version", "fm_status_str", "fm_gemm", "fm_ag_gemm", "fm_ag_gemm_p
            "fm_moe_gather_gemm_act",
            "fm_moe_ag_gather_gemm",
            "fm_moe_ag_gather_gemm_producers", "fm_moe_ag_gather_gemm_pull",
-           "fm_moe_gemm_scatter", "fm_moe_gemm_scatter_noalloc", "fm_probe_mfma")
+           "fm_moe_gemm_scatter", "fm_moe_gemm_scatter_noalloc", "fm_probe_mfma",
+           "fm_moe_gate_workspace_bytes", "fm_moe_gate", "fm_moe_gate_bwd",
+           "fm_norm_residual", "fm_norm_residual_workspace_bytes", "fm_norm_residual_bwd",
+           "fm_w4_row_bytes", "fm_w4_pack", "fm_gemm_w4", "fm_moe_gather_gemm_w4",
+           "fm_moe_w4_workspace_bytes", "fm_moe_gemm_scatter_w4")
 
 # fm_act_t: activation of MoE layer 0's result (fm_moe_gather_gemm_act)
 FM_ACT_NONE, FM_ACT_RELU, FM_ACT_GELU_TANH, FM_ACT_SILU = 0, 1, 2, 3
+# fm_gate_score_t: the router's scores (fm_moe_gate)
+FM_GATE_SOFTMAX, FM_GATE_SIGMOID = 0, 1
 
 
 class FluxMIError(RuntimeError):
@@ -103,6 +109,37 @@ def lib() -> ctypes.CDLL:
     L.fm_moe_gemm_scatter_noalloc.restype = ctypes.c_int
     L.fm_moe_gemm_scatter_noalloc.argtypes = [ctypes.c_int, i64, i64, i64, i32, i32, p, p, p, p,
                                               p, p, p, i64, p]
+    f32 = ctypes.c_float
+    L.fm_moe_gate_workspace_bytes.restype = sz
+    L.fm_moe_gate_workspace_bytes.argtypes = [i64, i32]
+    L.fm_moe_gate.restype = ctypes.c_int
+    L.fm_moe_gate.argtypes = [ctypes.c_int, i64, i32, i32, ctypes.c_int, i32, f32, p, p, p, p, p,
+                              p, p, p, p, sz, p]
+    L.fm_moe_gate_bwd.restype = ctypes.c_int
+    L.fm_moe_gate_bwd.argtypes = [ctypes.c_int, i64, i32, i32, ctypes.c_int, i32, f32, p, p, p, p,
+                                  p, p, p, p]
+    L.fm_norm_residual.restype = ctypes.c_int
+    L.fm_norm_residual.argtypes = [ctypes.c_int] * 3 + [i64, i64, p, p, p, p, p, i64, f32, f32, p,
+                                                        p, p, p, p]
+    L.fm_norm_residual_workspace_bytes.restype = sz
+    L.fm_norm_residual_workspace_bytes.argtypes = [i64, i64, i64]
+    L.fm_norm_residual_bwd.restype = ctypes.c_int
+    L.fm_norm_residual_bwd.argtypes = [ctypes.c_int] * 3 + [i64, i64, p, p, p, p, p, p, p, i64,
+                                                            f32, p, p, p, p, p, p, p, p, sz, p]
+    L.fm_w4_row_bytes.restype = sz
+    L.fm_w4_row_bytes.argtypes = [i64]
+    L.fm_w4_pack.restype = ctypes.c_int
+    L.fm_w4_pack.argtypes = [i64, i64, i64, p, p, p]
+    L.fm_gemm_w4.restype = ctypes.c_int
+    L.fm_gemm_w4.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, i32, p, p, p, p, p, p]
+    L.fm_moe_gather_gemm_w4.restype = ctypes.c_int
+    L.fm_moe_gather_gemm_w4.argtypes = [ctypes.c_int, i64, i64, i64, i32, i32, i32, i32, p, p, p,
+                                        p, p, p, p, p, ctypes.c_int, p, sz, p]
+    L.fm_moe_w4_workspace_bytes.restype = sz
+    L.fm_moe_w4_workspace_bytes.argtypes = [i64, i32, i64]
+    L.fm_moe_gemm_scatter_w4.restype = ctypes.c_int
+    L.fm_moe_gemm_scatter_w4.argtypes = [ctypes.c_int, i64, i64, i64, i32, i32, i32, i32, p, p, p,
+                                         p, p, p, p, p, p, p, p, sz, p]
     _lib = L
     return L
 
@@ -449,3 +486,260 @@ def fm_probe_mfma(dtype, mfma16: bool, waves_per_simd: int, iters: int, zero: bo
                                                 int(iters), int(bool(zero)), _ptr(out),
                                                 out.numel() * out.element_size() // 8,
                                                 _stream(stream)))
+
+
+# -- around the block: router, norms, 4-bit weights --------------------------------
+
+def _args(fn: str, *checks):
+    """Pointers of (name, tensor or None, dtype, shape) checks; all tensors have
+    to be contiguous and on the current device, whose stream the call goes to."""
+    device = _torch().cuda.current_device()
+    out = []
+    for name, t, dtype, shape in checks:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{fn}: {name} must be {dtype} {tuple(shape)}, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        if not t.is_cuda or t.device.index != device:
+            raise ValueError(f"{fn}: {name} must live on the current GPU")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _scratch(fn: str, n: int, device):
+    torch = _torch()
+    if n <= 0:
+        raise ValueError(f"{fn}: arguments out of range")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def fm_moe_gate_workspace_bytes(T: int, n_experts: int) -> int:
+    """Bytes of scratch that fm_moe_gate needs for its counts and loss."""
+    return int(lib().fm_moe_gate_workspace_bytes(int(T), int(n_experts)))
+
+
+def moe_gate_workspace(T: int, n_experts: int, device="cuda:0"):
+    """A uint8 device tensor of fm_moe_gate_workspace_bytes bytes."""
+    return _scratch("fm_moe_gate_workspace_bytes", fm_moe_gate_workspace_bytes(T, n_experts),
+                    device)
+
+
+def fm_moe_gate(logits, topk_ids, topk_weights, score: int = FM_GATE_SOFTMAX,
+                renormalize: bool = False, scale: float = 1.0, bias=None, token_mask=None,
+                counts=None, prob_sums=None, loss=None, ws=None, stream=None) -> None:
+    """topk_ids, topk_weights [T, topk] from logits [T, E]; with counts [E + 1],
+    prob_sums [E] and loss [1] (all or none) the expert counts and balance loss."""
+    torch = _torch()
+    T, E = logits.shape
+    topk = topk_ids.shape[1]
+    i32, f32 = torch.int32, torch.float32
+    x, b, m, ids, w, c, s, l = _args(
+        "fm_moe_gate", ("logits", logits, logits.dtype, (T, E)), ("bias", bias, f32, (E,)),
+        ("token_mask", token_mask, torch.uint8, (T,)), ("topk_ids", topk_ids, i32, (T, topk)),
+        ("topk_weights", topk_weights, f32, (T, topk)), ("counts", counts, i32, (E + 1,)),
+        ("prob_sums", prob_sums, f32, (E,)), ("loss", loss, f32, (1,)))
+    wp, wn = _ws(ws)
+    _check("fm_moe_gate", lib().fm_moe_gate(_dt(logits), T, E, topk, int(score),
+                                            int(bool(renormalize)), float(scale), x, b, m, ids, w,
+                                            c, s, l, wp, wn, _stream(stream)))
+
+
+def fm_moe_gate_bwd(logits, topk_ids, d_logits, score: int = FM_GATE_SOFTMAX,
+                    renormalize: bool = False, scale: float = 1.0, token_mask=None,
+                    d_weights=None, counts=None, d_loss=None, stream=None) -> None:
+    """d_logits [T, E] from d_weights [T, topk] (gradient of topk_weights) and
+    d_loss [1] (gradient of the loss, with fm_moe_gate's counts)."""
+    torch = _torch()
+    T, E = logits.shape
+    topk = topk_ids.shape[1]
+    i32, f32 = torch.int32, torch.float32
+    x, m, ids, dw, c, dl, dx = _args(
+        "fm_moe_gate_bwd", ("logits", logits, logits.dtype, (T, E)),
+        ("token_mask", token_mask, torch.uint8, (T,)), ("topk_ids", topk_ids, i32, (T, topk)),
+        ("d_weights", d_weights, f32, (T, topk)), ("counts", counts, i32, (E + 1,)),
+        ("d_loss", d_loss, f32, (1,)), ("d_logits", d_logits, logits.dtype, (T, E)))
+    _check("fm_moe_gate_bwd", lib().fm_moe_gate_bwd(
+        _dt(logits), T, E, topk, int(score), int(bool(renormalize)), float(scale), x, m, ids, dw,
+        c, dl, dx, _stream(stream)))
+
+
+def fm_norm_residual(out, y, block=None, resid=None, w_post=None, w_pre=None, gate=None,
+                     scale: float = 1.0, eps: float = 1e-6, rstd_post=None, rstd_pre=None,
+                     stream=None) -> None:
+    """out = resid + scale * gate * (norm(block) * w_post), y = norm(out) * w_pre;
+    out or y may be None (not wanted), as may every operand (see fluxmi.h)."""
+    torch = _torch()
+    like = next((t for t in (block, resid) if t is not None), None)
+    if like is None or (out is None and y is None):
+        raise ValueError("fm_norm_residual: block or resid, and out or y, are needed")
+    M, N = like.shape
+    sd = next((t.dtype for t in (resid, out) if t is not None), None)
+    dt = next((t.dtype for t in (y, w_pre, w_post, gate) if t is not None), None)
+    if dt is None:   # no 16-bit operand but the arrays themselves
+        dt = next((t.dtype for t in (resid, out, block)
+                   if t is not None and t.dtype != torch.float32), torch.bfloat16)
+    bd = block.dtype if block is not None else dt
+    sd = dt if sd is None else sd
+    G = gate.shape[0] if gate is not None else 0
+    f32 = torch.float32
+    b, r, wq, wp, g, o, yy, rq, rp = _args(
+        "fm_norm_residual", ("block", block, bd, (M, N)), ("resid", resid, sd, (M, N)),
+        ("w_post", w_post, dt, (N,)), ("w_pre", w_pre, dt, (N,)), ("gate", gate, dt, (G, N)),
+        ("out", out, sd, (M, N)), ("y", y, dt, (M, N)), ("rstd_post", rstd_post, f32, (M,)),
+        ("rstd_pre", rstd_pre, f32, (M,)))
+    _check("fm_norm_residual", lib().fm_norm_residual(
+        _DT(dt), _DT(sd), _DT(bd), M, N, b, r, wq, wp, g, G, float(scale), float(eps), o, yy, rq,
+        rp, _stream(stream)))
+
+
+def _DT(dtype) -> int:
+    torch = _torch()
+    try:
+        return {torch.float16: FM_F16, torch.bfloat16: FM_BF16, torch.float32: FM_F32}[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype}") from None
+
+
+def fm_norm_residual_workspace_bytes(M: int, N: int, n_gates: int = 0) -> int:
+    """Bytes of scratch that fm_norm_residual_bwd needs for its column sums."""
+    return int(lib().fm_norm_residual_workspace_bytes(int(M), int(N), int(n_gates)))
+
+
+def norm_residual_workspace(M: int, N: int, n_gates: int = 0, device="cuda:0"):
+    """A uint8 device tensor of fm_norm_residual_workspace_bytes bytes."""
+    return _scratch("fm_norm_residual_workspace_bytes",
+                    fm_norm_residual_workspace_bytes(M, N, n_gates), device)
+
+
+def fm_norm_residual_bwd(d_resid, d_block, out=None, block=None, d_y=None, d_out=None,
+                         w_post=None, w_pre=None, gate=None, scale: float = 1.0, rstd_post=None,
+                         rstd_pre=None, d_w_post=None, d_w_pre=None, d_gate=None, ws=None,
+                         stream=None) -> None:
+    """Gradients of fm_norm_residual; each of d_resid, d_block, d_w_post,
+    d_w_pre and d_gate may be None (not wanted)."""
+    torch = _torch()
+    like = next((t for t in (d_y, d_out) if t is not None), None)
+    if like is None:
+        raise ValueError("fm_norm_residual_bwd: d_y or d_out is needed")
+    M, N = like.shape
+    f32 = torch.float32
+    dt = next((t.dtype for t in (d_y, w_pre, w_post, gate) if t is not None), None)
+    if dt is None:
+        dt = next((t.dtype for t in (d_out, d_resid, block, d_block)
+                   if t is not None and t.dtype != f32), torch.bfloat16)
+    sd = next((t.dtype for t in (d_out, out, d_resid) if t is not None), dt)
+    bd = next((t.dtype for t in (block, d_block) if t is not None), dt)
+    G = gate.shape[0] if gate is not None else 0
+    dy, do, o, b, wq, wp, g, rq, rp, dr, db, dwq, dwp, dg = _args(
+        "fm_norm_residual_bwd", ("d_y", d_y, dt, (M, N)), ("d_out", d_out, sd, (M, N)),
+        ("out", out, sd, (M, N)), ("block", block, bd, (M, N)), ("w_post", w_post, dt, (N,)),
+        ("w_pre", w_pre, dt, (N,)), ("gate", gate, dt, (G, N)), ("rstd_post", rstd_post, f32, (M,)),
+        ("rstd_pre", rstd_pre, f32, (M,)), ("d_resid", d_resid, sd, (M, N)),
+        ("d_block", d_block, bd, (M, N)), ("d_w_post", d_w_post, f32, (N,)),
+        ("d_w_pre", d_w_pre, f32, (N,)), ("d_gate", d_gate, f32, (G, N)))
+    wsp, wsn = _ws(ws)
+    _check("fm_norm_residual_bwd", lib().fm_norm_residual_bwd(
+        _DT(dt), _DT(sd), _DT(bd), M, N, dy, do, o, b, wq, wp, g, G, float(scale), rq, rp, dr, db,
+        dwq, dwp, dg, wsp, wsn, _stream(stream)))
+
+
+def fm_w4_row_bytes(K: int) -> int:
+    """Packed bytes of one column of a 4-bit matrix with K rows."""
+    return int(lib().fm_w4_row_bytes(int(K)))
+
+
+def fm_w4_pack(codes, packed, stream=None) -> None:
+    """Codes uint8 [..., K, N] (0..15) into packed uint8 [..., N, fm_w4_row_bytes(K)]."""
+    torch = _torch()
+    lead, (K, N) = tuple(codes.shape[:-2]), codes.shape[-2:]
+    n = 1
+    for d in lead:
+        n *= d
+    c, p = _args("fm_w4_pack", ("codes", codes, torch.uint8, codes.shape),
+                 ("packed", packed, torch.uint8, lead + (N, fm_w4_row_bytes(K))))
+    _check("fm_w4_pack", lib().fm_w4_pack(n, K, N, c, p, _stream(stream)))
+
+
+def _w4_args(fn, x, packed, scales, zeros, lead, K, N, group):
+    """Pointers of a 4-bit operand of `lead` [K, N] matrices."""
+    if group not in (32, 64, 128):
+        raise ValueError(f"{fn}: group must be 32, 64 or 128")
+    u8 = _torch().uint8
+    shape = lead + (-(-K // group), N)
+    return _args(fn, ("x", x, x.dtype, x.shape),
+                 ("packed", packed, u8, lead + (N, -(-K // 128) * 64)),
+                 ("scales", scales, x.dtype, shape), ("zeros", zeros, u8, shape))
+
+
+def fm_gemm_w4(A, packed, scales, C, group: int, zeros=None, stream=None) -> None:
+    """C = A @ W, W [K, N] held as 4-bit codes with scales [ceil(K / group), N]
+    (and zeros of that shape, 8 without them)."""
+    M, K = A.shape
+    N = C.shape[1]
+    if C.shape[0] != M:
+        raise ValueError("fm_gemm_w4: shape mismatch")
+    a, w, s, z = _w4_args("fm_gemm_w4", A, packed, scales, zeros, (), K, N, group)
+    c, = _args("fm_gemm_w4", ("C", C, C.dtype, (M, N)))
+    _check("fm_gemm_w4", lib().fm_gemm_w4(_dt(A), _dt(C), M, N, K, int(group), a, w, s, z, c,
+                                          _stream(stream)))
+
+
+def fm_moe_gather_gemm_w4(X, topk_ids, packed, scales, H, sorted_pairs, expert_offsets,
+                          expert_begin: int, group: int, ws, zeros=None, act: int = FM_ACT_NONE,
+                          stream=None) -> None:
+    """Route, then H[rows of expert e] = act(X[gathered tokens] @ W1[e]), W1
+    [n_local, hidden, ffn] in 4 bits."""
+    torch = _torch()
+    T, hidden = X.shape
+    topk, ffn, n_local = topk_ids.shape[1], H.shape[1], packed.shape[0]
+    if H.shape[0] < T * topk or sorted_pairs.numel() < T * topk:
+        raise ValueError("fm_moe_gather_gemm_w4: H or sorted_pairs is too short")
+    x, w, s, z = _w4_args("fm_moe_gather_gemm_w4", X, packed, scales, zeros, (n_local,), hidden,
+                          ffn, group)
+    ids, h, sp, off = _args(
+        "fm_moe_gather_gemm_w4", ("topk_ids", topk_ids, torch.int32, (T, topk)),
+        ("H", H, X.dtype, H.shape), ("sorted_pairs", sorted_pairs, torch.int32, sorted_pairs.shape),
+        ("expert_offsets", expert_offsets, torch.int32, (n_local + 1,)))
+    wp, wn = _ws(ws)
+    _check("fm_moe_gather_gemm_w4", lib().fm_moe_gather_gemm_w4(
+        _dt(X), T, hidden, ffn, topk, int(expert_begin), n_local, int(group), x, ids, w, s, z, h,
+        sp, off, int(act), wp, wn, _stream(stream)))
+
+
+def fm_moe_w4_workspace_bytes(T: int, topk: int, hidden: int) -> int:
+    """Bytes of scratch that fm_moe_gemm_scatter_w4 needs."""
+    return int(lib().fm_moe_w4_workspace_bytes(int(T), int(topk), int(hidden)))
+
+
+def moe_w4_workspace(T: int, topk: int, hidden: int, device="cuda:0"):
+    """A uint8 device tensor of fm_moe_w4_workspace_bytes bytes."""
+    return _scratch("fm_moe_w4_workspace_bytes", fm_moe_w4_workspace_bytes(T, topk, hidden),
+                    device)
+
+
+def fm_moe_gemm_scatter_w4(H, packed, scales, topk_ids, sorted_pairs, expert_offsets,
+                           topk_weights, out, expert_begin: int, group: int, ws, zeros=None,
+                           add=None, stream=None) -> None:
+    """out[t] = add[t] + sum_k w[t,k] * (H[row(t,k)] @ W2[e(t,k)]) over local
+    pairs, W2 [n_local, ffn, hidden] in 4 bits."""
+    torch = _torch()
+    T, topk = topk_weights.shape
+    hidden, ffn, n_local = out.shape[1], H.shape[1], packed.shape[0]
+    if H.shape[0] < T * topk or sorted_pairs.numel() < T * topk:
+        raise ValueError("fm_moe_gemm_scatter_w4: H or sorted_pairs is too short")
+    h, w, s, z = _w4_args("fm_moe_gemm_scatter_w4", H, packed, scales, zeros, (n_local,), ffn,
+                          hidden, group)
+    ids, sp, off, tw, ad, o = _args(
+        "fm_moe_gemm_scatter_w4", ("topk_ids", topk_ids, torch.int32, (T, topk)),
+        ("sorted_pairs", sorted_pairs, torch.int32, sorted_pairs.shape),
+        ("expert_offsets", expert_offsets, torch.int32, (n_local + 1,)),
+        ("topk_weights", topk_weights, torch.float32, (T, topk)),
+        ("add", add, torch.float32, (T, hidden)), ("out", out, torch.float32, (T, hidden)))
+    wp, wn = _ws(ws)
+    _check("fm_moe_gemm_scatter_w4", lib().fm_moe_gemm_scatter_w4(
+        _dt(H), T, hidden, ffn, topk, int(expert_begin), n_local, int(group), h, w, s, z, ids, sp,
+        off, tw, ad, o, wp, wn, _stream(stream)))

@@ -1,0 +1,654 @@
+// fm_gate.hip -- the router of an MoE layer: logits -> experts and weights of
+// each token, expert counts and balance loss, and their gradient.
+//
+// A row of E logits lies in the registers of a group of LPR lanes, V a lane, so
+// one load of the row serves the choice, the softmax and the balance sums (the
+// operator moves little more than the logits).  Softmax statistics and weights
+// are fp32; the keys of a biased choice are fp64, because a rounded score next
+// to another one would change which experts are taken.
+#include <algorithm>
+
+#include "fm_wave.hpp"
+
+namespace fm {
+namespace {
+
+constexpr int kGateThreads = 256;
+constexpr int kGateWaves = kGateThreads / 64;
+constexpr int kGateMaxExperts = 1024;
+constexpr int kGateMaxTopk = 16;
+constexpr int kGateMaxBlocks = 512;     // blocks whose partial sums are joined
+constexpr int kGateFinishThreads = 1024;
+constexpr float kNegInf = -__builtin_inff();
+
+// exp(x) for x <= 0 (or NaN): 1 ulp of exp2 plus the argument's rounding.
+__device__ __forceinline__ float exp_neg(float x) { return __expf(x); }
+
+// LDS traffic between the lanes of one wave: the wave's LDS operations complete
+// in order, so only the compiler has to keep them so.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// sigmoid(x) * exp(-m) with m <= 0: for shares and renormalised weights, which
+// do not change with m; m near the largest min(x, 0) keeps them from vanishing.
+__device__ __forceinline__ float sigmoid_num(float x, float m) {
+  return exp_neg(fminf(x, 0.f) - m) / (1.f + exp_neg(-fabsf(x)));
+}
+
+// The expert of slot v of a lane: V / 4 chunks of 4, chunk c at (c * LPR + sub) * 4.
+template <int LPR>
+__device__ __forceinline__ int slot_expert(int v, int sub) {
+  return ((v >> 2) * LPR + sub) * 4 + (v & 3);
+}
+
+template <typename E, int LPR, int V>
+__device__ __forceinline__ void load_row(const typename Elem<E>::type* row, int n, int sub,
+                                         float (&x)[V]) {
+  if (n % 4 == 0) {   // rows start on a 4-element boundary
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) {
+      const int e = (c * LPR + sub) * 4;
+      f32x4 q = {kNegInf, kNegInf, kNegInf, kNegInf};
+      if (e < n) q = widen<E>(*reinterpret_cast<const typename Raw4<E>::type*>(row + e));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[c * 4 + i] = q[i];
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = slot_expert<LPR>(v, sub);
+      x[v] = e < n ? (float)row[e] : kNegInf;
+    }
+  }
+}
+
+struct GateArgs {
+  const void* logits;
+  const float* bias;
+  const uint8_t* mask;
+  int32_t* ids;
+  float* weights;
+  int32_t* counts;
+  float* sums;
+  float* loss;
+  float* part_sums;      // [blocks, E]
+  int32_t* part_counts;  // [blocks, E + 1]
+  int64_t T;
+  int E, topk;
+  int sigmoid, renorm, stats;
+  float scale;
+};
+
+// counts, sums and loss from (sum, count) of each expert and the token count.
+// Every thread of the block calls it; s_loss holds one double a wave.
+template <typename Get>
+__device__ __forceinline__ void gate_finish(const GateArgs& a, int n, Get get, double* s_loss) {
+  const int t = threadIdx.x, waves = blockDim.x / 64;
+  double dot = 0;
+  for (int e = t; e < a.E; e += blockDim.x) {
+    float sum;
+    int cnt;
+    get(e, sum, cnt);
+    a.sums[e] = sum;
+    a.counts[e] = cnt;
+    dot += (double)sum * cnt;
+  }
+  dot = group_sum<64>(dot);
+  if (t % 64 == 0) s_loss[t / 64] = dot;
+  __syncthreads();
+  if (t == 0) {
+    double all = 0;
+    for (int w = 0; w < waves; ++w) all += s_loss[w];
+    const double nn = n > 0 ? (double)n : 1.0;
+    a.counts[a.E] = n;
+    a.loss[0] = (float)(all * a.E / (a.topk * nn * nn));
+  }
+}
+
+template <typename E, int LPR, int V, bool BIAS>
+__global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
+  constexpr int G = 64 / LPR;             // rows of a wave
+  constexpr int RP = G * kGateWaves;      // rows of a block and pass
+  __shared__ float s_x[RP][kGateMaxTopk];
+  __shared__ int s_id[RP][kGateMaxTopk];
+  __shared__ float s_m[RP], s_inv[RP];
+  __shared__ int s_cnt[LPR * V + 1];
+  __shared__ float s_sum[RP * LPR * V];
+  __shared__ double s_loss[kGateWaves];
+  typedef typename std::conditional<BIAS, double, float>::type Key;
+
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int sub = lane % LPR, grp = lane / LPR, r = wave * G + grp;
+  const int n = a.E, topk = a.topk;
+  if (a.stats) {
+    for (int e = t; e <= n; e += kGateThreads) s_cnt[e] = 0;
+    __syncthreads();
+  }
+  float bias[V], acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    acc[v] = 0.f;
+    const int e = slot_expert<LPR>(v, sub);
+    bias[v] = BIAS && e < n ? a.bias[e] : 0.f;
+  }
+  int tokens = 0;
+  for (int64_t base = (int64_t)blockIdx.x * RP; base < a.T; base += (int64_t)gridDim.x * RP) {
+    const int64_t row = base + r;
+    const bool live = row < a.T && (!a.mask || a.mask[row] != 0);
+    float x[V];
+    if (live) {
+      load_row<E, LPR, V>(static_cast<const typename Elem<E>::type*>(a.logits) + row * n, n, sub, x);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = kNegInf;
+    }
+    if (a.stats || !a.sigmoid) {
+      float m = x[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
+      m = group_max<LPR>(m);
+      if (m == kNegInf) m = 0.f;          // every share becomes 0
+      if (a.sigmoid) m = fminf(m, 0.f);
+      float p[V], sum = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        p[v] = a.sigmoid ? sigmoid_num(x[v], m) : exp_neg(x[v] - m);
+        sum += p[v];
+      }
+      sum = group_sum<LPR>(sum);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += p[v] * inv;
+      if (sub == 0) {
+        s_m[r] = m;
+        s_inv[r] = inv;
+      }
+    }
+    Key key[V];
+    if constexpr (BIAS) {
+      if (a.sigmoid) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = 1.0 / (1.0 + exp(-(double)x[v]));
+      } else {
+        double m = (double)x[0], sum = 0;
+#pragma unroll
+        for (int v = 1; v < V; ++v) m = fmax(m, (double)x[v]);
+        m = (double)group_max<LPR>((float)m);
+        if (m == -__builtin_inf()) m = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          key[v] = exp((double)x[v] - m);
+          sum += key[v];
+        }
+        sum = group_sum<LPR>(sum);
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = sum == 0 ? 0.0 : key[v] / sum;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        key[v] = x[v] == kNegInf ? (Key)kNegInf : key[v] + (Key)bias[v];
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = x[v];
+    }
+    // topk times the largest key that is left; of equal ones the lowest expert.
+    for (int k = 0; k < topk; ++k) {
+      Key best = (Key)kNegInf;
+      int at = 0x7fffffff;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (key[v] > best) {
+          best = key[v];
+          at = slot_expert<LPR>(v, sub);
+        }
+      auto join = [&](auto step) {
+        constexpr int STEP = decltype(step)::value;
+        if constexpr (STEP < LPR) {
+          const LanePair<Key> pk = lane_pair<STEP>(best);
+          const LanePair<int> pe = lane_pair<STEP>(at);
+          const bool b = pk.b > pk.a || (pk.b == pk.a && pe.b < pe.a);
+          best = b ? pk.b : pk.a;
+          at = b ? pe.b : pe.a;
+        }
+      };
+      join(std::integral_constant<int, 1>());
+      join(std::integral_constant<int, 2>());
+      join(std::integral_constant<int, 4>());
+      join(std::integral_constant<int, 8>());
+      join(std::integral_constant<int, 16>());
+      join(std::integral_constant<int, 32>());
+      if (best == (Key)kNegInf) at = -1;
+      const int rel = at - sub * 4;
+      float mine = kNegInf;
+      bool own = false;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const bool hit = at >= 0 && rel == (v >> 2) * LPR * 4 + (v & 3);
+        mine = hit ? x[v] : mine;
+        own = own || hit;
+        key[v] = hit ? (Key)kNegInf : key[v];
+      }
+      if (own) s_x[r][k] = mine;
+      if (sub == 0) s_id[r][k] = at;
+    }
+    wave_lds_sync();
+    tokens += live && sub == 0;
+    for (int i = lane; i < G * topk; i += 64) {
+      const int q = wave * G + i / topk, k = i % topk;
+      const int64_t to = base + q;
+      if (to >= a.T) continue;
+      const int id = s_id[q][k];
+      float w = 0.f;
+      if (id >= 0) {
+        const float xk = s_x[q][k];
+        if (a.renorm) {
+          float m = kNegInf, sum = 0.f;
+          for (int j = 0; j < topk; ++j) m = s_id[q][j] >= 0 ? fmaxf(m, s_x[q][j]) : m;
+          if (a.sigmoid) m = fminf(m, 0.f);
+          for (int j = 0; j < topk; ++j)
+            if (s_id[q][j] >= 0)
+              sum += a.sigmoid ? sigmoid_num(s_x[q][j], m) : exp_neg(s_x[q][j] - m);
+          w = (a.sigmoid ? sigmoid_num(xk, m) : exp_neg(xk - m)) / sum;
+        } else {
+          w = a.sigmoid ? sigmoid_num(xk, 0.f) : exp_neg(xk - s_m[q]) * s_inv[q];
+        }
+        w *= a.scale;
+        if (a.stats) atomicAdd(&s_cnt[id], 1);
+      }
+      a.ids[to * topk + k] = id;
+      a.weights[to * topk + k] = w;
+    }
+    wave_lds_sync();
+  }
+  if (!a.stats) return;
+  tokens = group_sum<64>(tokens);
+  if (lane == 0) atomicAdd(&s_cnt[n], tokens);
+#pragma unroll
+  for (int v = 0; v < V; ++v) s_sum[r * LPR * V + slot_expert<LPR>(v, sub)] = acc[v];
+  __syncthreads();
+  auto block_sum = [&](int e) {
+    float s = 0.f;
+    for (int q = 0; q < RP; ++q) s += s_sum[q * LPR * V + e];
+    return s;
+  };
+  if (gridDim.x == 1) {
+    gate_finish(a, s_cnt[n], [&](int e, float& sum, int& cnt) {
+      sum = block_sum(e);
+      cnt = s_cnt[e];
+    }, s_loss);
+  } else {
+    for (int e = t; e < n; e += kGateThreads) {
+      a.part_sums[(int64_t)blockIdx.x * n + e] = block_sum(e);
+    }
+    for (int e = t; e <= n; e += kGateThreads)
+      a.part_counts[(int64_t)blockIdx.x * (n + 1) + e] = s_cnt[e];
+  }
+}
+
+// Joins the blocks' partial sums: S threads an expert, each over every S-th
+// block, then the S parts in order.
+__global__ __launch_bounds__(kGateFinishThreads) void gate_join(const GateArgs a, int blocks) {
+  __shared__ float s_sum[kGateFinishThreads];
+  __shared__ int s_cnt[kGateFinishThreads];
+  __shared__ int s_n;
+  __shared__ double s_loss[kGateFinishThreads / 64];
+  const int t = threadIdx.x, E = a.E;
+  const int S = std::max(1, kGateFinishThreads / E);
+  if (t == 0) s_n = 0;
+  __syncthreads();
+  float sum = 0.f;
+  int cnt = 0;
+  if (t < S * E) {
+    const int e = t % E;
+#pragma unroll 8
+    for (int b = t / E; b < blocks; b += S) {
+      sum += a.part_sums[(int64_t)b * E + e];
+      cnt += a.part_counts[(int64_t)b * (E + 1) + e];
+    }
+  }
+  s_sum[t] = sum;
+  s_cnt[t] = cnt;
+  int tokens = 0;
+  for (int b = t; b < blocks; b += kGateFinishThreads) tokens += a.part_counts[(int64_t)b * (E + 1) + E];
+  if (tokens) atomicAdd(&s_n, tokens);
+  __syncthreads();
+  gate_finish(a, s_n, [&](int e, float& s, int& c) {
+    s = 0.f;
+    c = 0;
+    for (int j = 0; j < S; ++j) {
+      s += s_sum[j * E + e];
+      c += s_cnt[j * E + e];
+    }
+  }, s_loss);
+}
+
+struct GateBwdArgs {
+  const void* logits;
+  const uint8_t* mask;
+  const int32_t* ids;
+  const float* d_weights;
+  const int32_t* counts;
+  const float* d_loss;
+  void* d_logits;
+  int64_t T;
+  int E, topk;
+  int sigmoid, renorm;
+  float scale;
+};
+
+// With u, share p and the chosen slots' gradients d_k = scale * d_weights:
+//   du = p * (a - sum p a) + slots,      a = d_loss * E / (topk n^2) * counts
+//   slots: q_k (d_k - sum q d), q = softmax of u over the chosen (renormalised);
+//          w_k d_k, less p * sum w d for a softmax score
+//   dx = du (softmax) or du * sigmoid(-x).
+template <typename E, int LPR, int V>
+__global__ __launch_bounds__(kGateThreads) void gate_bwd(const GateBwdArgs a) {
+  typedef typename Elem<E>::type L;
+  constexpr int G = 64 / LPR;
+  constexpr int RP = G * kGateWaves;
+  __shared__ float s_x[RP][kGateMaxTopk], s_d[RP][kGateMaxTopk], s_c[RP][kGateMaxTopk];
+  __shared__ int s_id[RP][kGateMaxTopk];
+  __shared__ float s_m[RP], s_inv[RP];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int sub = lane % LPR, grp = lane / LPR, r = wave * G + grp;
+  const int n = a.E, topk = a.topk;
+  const L* logits = static_cast<const L*>(a.logits);
+  float ae[V];
+  {
+    float coef = 0.f;
+    if (a.counts) {
+      const double nn = (double)a.counts[n];
+      coef = nn > 0 ? (float)((double)a.d_loss[0] * n / (topk * nn * nn)) : 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = slot_expert<LPR>(v, sub);
+      ae[v] = a.counts && e < n ? coef * (float)a.counts[e] : 0.f;
+    }
+  }
+  for (int64_t base = (int64_t)blockIdx.x * RP; base < a.T; base += (int64_t)gridDim.x * RP) {
+    const int64_t row = base + r;
+    const bool live = row < a.T && (!a.mask || a.mask[row] != 0);
+    float x[V];
+    if (live) {
+      load_row<E, LPR, V>(logits + row * n, n, sub, x);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = kNegInf;
+    }
+    // the slots' inputs
+    if (a.d_weights) {
+      for (int i = lane; i < G * topk; i += 64) {
+        const int q = wave * G + i / topk, k = i % topk;
+        const int64_t at = base + q;
+        const bool in = at < a.T && (!a.mask || a.mask[at] != 0);
+        int id = in ? a.ids[at * topk + k] : -1;
+        if ((unsigned)id >= (unsigned)n) id = -1;
+        s_id[q][k] = id;
+        s_x[q][k] = id >= 0 ? (float)logits[at * n + id] : kNegInf;
+        s_d[q][k] = id >= 0 ? a.d_weights[at * topk + k] * a.scale : 0.f;
+      }
+    }
+    float m = x[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
+    m = group_max<LPR>(m);
+    if (m == kNegInf) m = 0.f;
+    if (a.sigmoid) m = fminf(m, 0.f);
+    float p[V], sum = 0.f, dot = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      p[v] = a.sigmoid ? sigmoid_num(x[v], m) : exp_neg(x[v] - m);
+      sum += p[v];
+      dot += p[v] * ae[v];
+    }
+    sum = group_sum<LPR>(sum);
+    dot = group_sum<LPR>(dot);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    dot *= inv;
+    if (a.d_weights) {
+      if (sub == 0) {
+        s_m[r] = m;
+        s_inv[r] = inv;
+      }
+      wave_lds_sync();
+      for (int i = lane; i < G * topk; i += 64) {
+        const int q = wave * G + i / topk, k = i % topk;
+        float c = 0.f;
+        if (s_id[q][k] >= 0) {
+          const float xk = s_x[q][k], d = s_d[q][k];
+          if (a.renorm) {
+            float mw = kNegInf, sw = 0.f, dw = 0.f;
+            for (int j = 0; j < topk; ++j) mw = fmaxf(mw, s_x[q][j]);
+            if (mw == kNegInf) mw = 0.f;
+            if (a.sigmoid) mw = fminf(mw, 0.f);
+            for (int j = 0; j < topk; ++j) {
+              const float w = a.sigmoid ? sigmoid_num(s_x[q][j], mw) : exp_neg(s_x[q][j] - mw);
+              sw += w;
+              dw += w * s_d[q][j];
+            }
+            const float iw = sw == 0.f ? 0.f : 1.f / sw;
+            const float w = a.sigmoid ? sigmoid_num(xk, mw) : exp_neg(xk - mw);
+            c = w * iw * (d - dw * iw);
+          } else {
+            c = d * (a.sigmoid ? sigmoid_num(xk, 0.f) : exp_neg(xk - s_m[q]) * s_inv[q]);
+          }
+        }
+        s_c[q][k] = c;
+      }
+      wave_lds_sync();
+      if (!a.sigmoid && !a.renorm)
+        for (int k = 0; k < topk; ++k) dot += s_c[r][k];
+    }
+    float du[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) du[v] = p[v] * inv * (ae[v] - dot);
+    if (a.d_weights) {
+      for (int k = 0; k < topk; ++k) {
+        const int rel = s_id[r][k] - sub * 4;
+        const float c = s_c[r][k];
+#pragma unroll
+        for (int v = 0; v < V; ++v) du[v] += rel == (v >> 2) * LPR * 4 + (v & 3) ? c : 0.f;
+      }
+      wave_lds_sync();
+    }
+    if (a.sigmoid) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float ex = exp_neg(-fabsf(x[v]));
+        du[v] *= (x[v] > 0.f ? ex : 1.f) / (1.f + ex);
+      }
+    }
+    if (row < a.T) {
+      L* to = static_cast<L*>(a.d_logits) + row * n;
+#pragma unroll
+      for (int v = 0; v < V; ++v) du[v] = live && x[v] != kNegInf ? du[v] : 0.f;
+      if (n % 4 == 0) {
+#pragma unroll
+        for (int c = 0; c < V / 4; ++c) {
+          const int e = (c * LPR + sub) * 4;
+          if (e < n) {
+            const f32x4 q = {du[c * 4], du[c * 4 + 1], du[c * 4 + 2], du[c * 4 + 3]};
+            *reinterpret_cast<typename Raw4<E>::type*>(to + e) = narrow<E>(q);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int e = slot_expert<LPR>(v, sub);
+          if (e < n) to[e] = (L)du[v];
+        }
+      }
+    }
+  }
+}
+
+// Lanes of a row: the fewest that hold it with up to 16 experts a lane, so that
+// exchanges between lanes are few.
+int gate_lanes(int E) {
+  return E <= 32 ? 4 : E <= 64 ? 8 : E <= 256 ? 16 : E <= 512 ? 32 : 64;
+}
+
+int gate_blocks(int64_t T, int E) {
+  const int64_t rows = kGateThreads / gate_lanes(E);
+  const int64_t passes = cdiv(T, rows);
+  return (int)(passes <= 2 ? 1 : std::min<int64_t>(passes, kGateMaxBlocks));
+}
+
+size_t gate_ws(int64_t T, int E) {
+  return (size_t)cdiv((int64_t)gate_blocks(T, E) * (2 * E + 1) * 4, 256) * 256;
+}
+
+fm_status_t check_gate(fm_dtype_t dt, int64_t T, int E, int topk, int score, int renorm,
+                       const void* logits) {
+  if (dt != FM_F16 && dt != FM_BF16 && dt != FM_F32) return FM_ERR_UNSUPPORTED;
+  if (T < 0 || E < 1 || E > kGateMaxExperts || topk < 1 || topk > kGateMaxTopk || topk > E)
+    return FM_ERR_INVALID_ARG;
+  if ((score != FM_GATE_SOFTMAX && score != FM_GATE_SIGMOID) || renorm < 0 || renorm > 1)
+    return FM_ERR_INVALID_ARG;
+  if (T * topk >= (1ll << 31)) return FM_ERR_UNSUPPORTED;
+  if (T > 0 && (!logits || !aligned16(logits))) return FM_ERR_INVALID_ARG;
+  return FM_OK;
+}
+
+}  // namespace
+}  // namespace fm
+
+using namespace fm;
+
+#define FM_GATE_LANES(CALL, E)                  \
+  switch (gate_lanes(E)) {                      \
+    case 4: CALL(4, 8); break;                  \
+    case 8: CALL(8, 8); break;                  \
+    case 16:                                    \
+      if ((E) <= 128) CALL(16, 8);              \
+      else CALL(16, 16);                        \
+      break;                                    \
+    case 32: CALL(32, 16); break;               \
+    default: CALL(64, 16); break;               \
+  }
+
+extern "C" size_t fm_moe_gate_workspace_bytes(int64_t T, int32_t n_experts) {
+  if (T < 0 || n_experts < 1 || n_experts > kGateMaxExperts) return 0;
+  return gate_ws(T, n_experts);
+}
+
+extern "C" fm_status_t fm_moe_gate(fm_dtype_t dt, int64_t T, int32_t n_experts, int32_t topk,
+                                   fm_gate_score_t score, int32_t renormalize, float scale,
+                                   const void* logits, const float* bias,
+                                   const uint8_t* token_mask, int32_t* topk_ids,
+                                   float* topk_weights, int32_t* counts, float* prob_sums,
+                                   float* loss, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const fm_status_t st = check_gate(dt, T, n_experts, topk, score, renormalize, logits);
+  if (st != FM_OK) return st;
+  const bool stats = counts || prob_sums || loss;
+  if (T > 0 && (!topk_ids || !topk_weights)) return FM_ERR_INVALID_ARG;
+  if (!aligned4(topk_ids) || !aligned4(topk_weights) || !aligned4(bias) || !aligned4(counts) ||
+      !aligned4(prob_sums) || !aligned4(loss))
+    return FM_ERR_INVALID_ARG;
+  if (stats && (!counts || !prob_sums || !loss || !ws || !aligned16(ws) ||
+                ws_bytes < gate_ws(T, n_experts)))
+    return FM_ERR_INVALID_ARG;
+  if (T == 0 && !stats) return FM_OK;
+  GateArgs a = {};
+  a.logits = logits;
+  a.bias = bias;
+  a.mask = token_mask;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.counts = counts;
+  a.sums = prob_sums;
+  a.loss = loss;
+  a.T = T;
+  a.E = n_experts;
+  a.topk = topk;
+  a.sigmoid = score == FM_GATE_SIGMOID;
+  a.renorm = renormalize;
+  a.stats = stats;
+  a.scale = scale;
+  int blocks = gate_blocks(T, n_experts);
+  if (stats) {
+    a.part_sums = static_cast<float*>(ws);
+    a.part_counts = static_cast<int32_t*>(ws) + (int64_t)blocks * n_experts;
+  } else {
+    blocks = (int)std::min<int64_t>(cdiv(T, kGateThreads / gate_lanes(n_experts)), 4096);
+  }
+#define FM_GATE_CALL(LPR, V)                                                               \
+  do {                                                                                     \
+    if (bias)                                                                              \
+      hipLaunchKernelGGL((gate_fwd<FM_E, LPR, V, true>), dim3(blocks), dim3(kGateThreads), 0, \
+                         stream, a);                                                       \
+    else                                                                                   \
+      hipLaunchKernelGGL((gate_fwd<FM_E, LPR, V, false>), dim3(blocks), dim3(kGateThreads), 0, \
+                         stream, a);                                                       \
+  } while (0)
+  if (dt == FM_F16) {
+#define FM_E F16
+    FM_GATE_LANES(FM_GATE_CALL, n_experts)
+#undef FM_E
+  } else if (dt == FM_BF16) {
+#define FM_E BF16
+    FM_GATE_LANES(FM_GATE_CALL, n_experts)
+#undef FM_E
+  } else {
+#define FM_E F32
+    FM_GATE_LANES(FM_GATE_CALL, n_experts)
+#undef FM_E
+  }
+#undef FM_GATE_CALL
+  if (stats && blocks > 1)
+    hipLaunchKernelGGL(gate_join, dim3(1), dim3(kGateFinishThreads), 0, stream, a, blocks);
+  return launch_status();
+}
+
+extern "C" fm_status_t fm_moe_gate_bwd(fm_dtype_t dt, int64_t T, int32_t n_experts,
+                                       int32_t topk, fm_gate_score_t score, int32_t renormalize,
+                                       float scale, const void* logits,
+                                       const uint8_t* token_mask, const int32_t* topk_ids,
+                                       const float* d_weights, const int32_t* counts,
+                                       const float* d_loss, void* d_logits, hipStream_t stream) {
+  const fm_status_t st = check_gate(dt, T, n_experts, topk, score, renormalize, logits);
+  if (st != FM_OK) return st;
+  if ((counts == nullptr) != (d_loss == nullptr)) return FM_ERR_INVALID_ARG;
+  if (!aligned4(topk_ids) || !aligned4(d_weights) || !aligned4(counts) || !aligned4(d_loss))
+    return FM_ERR_INVALID_ARG;
+  if (T == 0) return FM_OK;
+  if (!d_logits || !aligned16(d_logits) || (d_weights && !topk_ids)) return FM_ERR_INVALID_ARG;
+  const int64_t bytes = T * n_experts * (dt == FM_F32 ? 4 : 2);
+  const char *x = static_cast<const char*>(logits), *y = static_cast<const char*>(d_logits);
+  if (x < y + bytes && y < x + bytes) return FM_ERR_INVALID_ARG;
+  GateBwdArgs a = {};
+  a.logits = logits;
+  a.mask = token_mask;
+  a.ids = topk_ids;
+  a.d_weights = d_weights;
+  a.counts = counts;
+  a.d_loss = d_loss;
+  a.d_logits = d_logits;
+  a.T = T;
+  a.E = n_experts;
+  a.topk = topk;
+  a.sigmoid = score == FM_GATE_SIGMOID;
+  a.renorm = renormalize;
+  a.scale = scale;
+  const int blocks = (int)std::min<int64_t>(cdiv(T, kGateThreads / gate_lanes(n_experts)), 2048);
+#define FM_GATE_CALL(LPR, V)                                                                  \
+  hipLaunchKernelGGL((gate_bwd<FM_E, LPR, V>), dim3(blocks), dim3(kGateThreads), 0, stream, a)
+  if (dt == FM_F16) {
+#define FM_E F16
+    FM_GATE_LANES(FM_GATE_CALL, n_experts)
+#undef FM_E
+  } else if (dt == FM_BF16) {
+#define FM_E BF16
+    FM_GATE_LANES(FM_GATE_CALL, n_experts)
+#undef FM_E
+  } else {
+#define FM_E F32
+    FM_GATE_LANES(FM_GATE_CALL, n_experts)
+#undef FM_E
+  }
+#undef FM_GATE_CALL
+  return launch_status();
+}
