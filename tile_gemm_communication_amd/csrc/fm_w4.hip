@@ -57,7 +57,7 @@ struct W4Args {
   const int32_t* pairs;
   const int32_t* offsets;
   const float* weights;
-  int64_t M;
+  int64_t M;     // rows of x
   int N, K;
   int blocks;    // 128-wide blocks of K
   int groups;
@@ -77,141 +77,357 @@ __device__ __forceinline__ float activate(float x, int act) {
   }
 }
 
-// What one step of 128 k reads: the lane's 32 codes, its rows' x, and the scale
-// and zero of its column's groups.
-template <typename E, int GB, int MT>
-struct W4Step {
-  u32x4 w;
-  u32x4 x[MT][4];
-  typename Elem<E>::type s[4 / GB];
-  uint8_t z[4 / GB];
+// The column tile of a block: each XCD (blocks go to them in turn) takes
+// neighbouring tiles, whose scales share cache lines.
+__device__ __forceinline__ int column_tile() {
+  const int b = blockIdx.x, n = gridDim.x, x = b & 7;
+  return x * (n >> 3) + min(x, n & 7) + (b >> 3);
+}
+
+// Loads go through buffer resources: the lane's 32-bit offset stays as it is and
+// the step's is a scalar, so that a load costs no address registers.  An offset
+// past the resource reads 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)(uint32_t)bytes,
+                                           kBufRsrcWord3);
+}
+
+// The weights of the columns from n0 of matrix e (up to 16 * NT of them), and the
+// scales and zeros of the matrix.
+struct W4Source {
+  __amdgpu_buffer_rsrc_t w, s, z;
 };
 
-// GB: 32-wide matrix instructions of a group.  A chunk of rows is MT * R * 4:
-// logical row (mt R + r) 4 + q is operand row 4 q + r, so that with few rows
-// only accumulator r < R of every lane is in use.  PF steps are in flight.
-template <typename E, int GB, int MT, int R, int PF, W4Mode MODE>
-__global__ __launch_bounds__(kW4Threads) void w4_product(const W4Args a) {
+template <bool Z>
+__device__ __forceinline__ W4Source source_of(const W4Args& a, int e, int n0, int columns) {
+  const int64_t row = (int64_t)a.blocks * 64, scales = (int64_t)a.groups * a.N;
+  const uint8_t* w = a.packed + ((int64_t)e * a.N + n0) * row;
+  return {resource(w, min(columns, a.N - n0) * row),
+          resource(static_cast<const char*>(a.scales) + e * scales * 2, scales * 2),
+          resource(Z ? a.zeros + e * scales : nullptr, Z ? scales : 0)};
+}
+
+__device__ __forceinline__ u32x4 load_codes(const W4Source& src, uint32_t lane_offset, int step) {
+  return __builtin_bit_cast(u32x4,
+                            __builtin_amdgcn_raw_buffer_load_b128(src.w, lane_offset, step * 64, 0));
+}
+
+// A loaded value where it is first used.  Without this the optimizer moves what
+// the loop's body and its remainder both compute from a load up to the load
+// itself, where it waits for the data and holds the wider result.
+__device__ __forceinline__ void loaded(u32x4& v) { asm volatile("" : "+v"(v)); }
+
+// Scales and zeros of one 16-column tile and step of 128 k.
+template <typename E, int GB, bool Z>
+struct W4Scales {
+  uint32_t s[4 / GB];            // the 16 bits of each scale
+  uint32_t z[Z ? 4 / GB : 1];
+  __device__ __forceinline__ void loaded() {
+#pragma unroll
+    for (int g = 0; g < 4 / GB; ++g) {
+      asm volatile("" : "+v"(s[g]));
+      if constexpr (Z) asm volatile("" : "+v"(z[g]));
+    }
+  }
+  __device__ __forceinline__ float scale(int g) const {
+    return (float)__builtin_bit_cast(typename Elem<E>::type, (uint16_t)s[g]);
+  }
+  // -(base + zero)
+  __device__ __forceinline__ float offset(int g) const {
+    return Z ? -code_base(E()) - (float)z[Z ? g : 0] : -code_base(E()) - 8.f;
+  }
+};
+
+// n: the lane's column.  Groups past the last repeat it; x is 0 there.
+template <typename E, int GB, bool Z>
+__device__ __forceinline__ void load_scales(W4Scales<E, GB, Z>& f, const W4Args& a,
+                                            const W4Source& src, uint32_t n, int step) {
+#pragma unroll
+  for (int g = 0; g < 4 / GB; ++g) {
+    const int row = min(step * (4 / GB) + g, a.groups - 1) * a.N;
+    f.s[g] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src.s, n * 2, row * 2, 0);
+    if constexpr (Z) f.z[g] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.z, n, row, 0);
+  }
+}
+
+template <W4Mode MODE>
+__device__ __forceinline__ int64_t x_row(const W4Args& a, int64_t first, int64_t m) {
+  return MODE == kGather ? a.pairs[first + m] / a.topk : first + m;
+}
+
+// Stores output (row m of the expert's, col) = v.
+template <typename E, W4Mode MODE>
+__device__ __forceinline__ void store_out(const W4Args& a, int64_t first, int64_t m, int col,
+                                          float v) {
   typedef typename Elem<E>::type L;
-  constexpr int GP = 4 / GB;
-  constexpr int ROWS = MT * R * 4;
-  __shared__ float s_part[kW4Waves][MT * R][64];
+  if (MODE == kScatter) {
+    const int64_t p = a.pairs[first + m];
+    static_cast<float*>(a.out)[p * a.N + col] = v * a.weights[p];
+  } else if (MODE == kDense32) {
+    static_cast<float*>(a.out)[m * a.N + col] = v;
+  } else {
+    if (MODE == kGather) v = activate(v, a.act);
+    static_cast<L*>(a.out)[(first + m) * a.N + col] = (L)v;
+  }
+}
+
+// Few rows (chunks of 4 R): a block owns 16 columns and its 8 waves share K in
+// contiguous parts.  x lies in LDS, so that the loads in flight are weights and
+// scales alone (memory loads complete in order: an x load behind them would
+// wait for them).  Logical row 4 r + i of a chunk is operand row 4 i + r, so that
+// only accumulators r < R of a lane are in use; operand rows without a logical
+// row repeat others, and what they give is not looked at.
+constexpr int kFewAhead = 4;   // steps of 128 k in flight
+
+template <typename E, int GB, bool Z, int R, W4Mode MODE>
+__global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_few(
+    const W4Args a) {
+  typedef typename Elem<E>::type L;
+  constexpr int ROWS = 4 * R, GP = 4 / GB, PF = kFewAhead;
+  __shared__ float s_part[kW4Waves][R][64];
+  extern __shared__ char s_x[];   // rows of stride bytes
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int i16 = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = column_tile() * 16;
   const int n = min(n0 + i16, a.N - 1);
   const int e = MODE == kGather || MODE == kScatter ? blockIdx.y : 0;
   int64_t first = 0, rows = a.M;
   if (MODE == kGather || MODE == kScatter) {
-    first = a.offsets[e];
-    rows = a.offsets[e + 1] - first;
+    first = __builtin_amdgcn_readfirstlane(a.offsets[e]);
+    rows = __builtin_amdgcn_readfirstlane(a.offsets[e + 1]) - first;
     if (rows <= 0) return;
   }
-  const uint8_t* wp = a.packed + ((int64_t)e * a.N + n) * a.blocks * 64 + q * 16;
-  const int64_t sbase = (int64_t)e * a.groups * a.N + n;
-  const L* sp = static_cast<const L*>(a.scales) + sbase;
-  const uint8_t* zp = a.zeros ? a.zeros + sbase : nullptr;
+  const int stride = a.blocks * 256 + 16;   // rows start 16 bytes apart in the banks
+  const W4Source src = source_of<Z>(a, e, n0, 16);
+  const uint32_t wo = (uint32_t)i16 * a.blocks * 64 + q * 16;   // columns past N read 0
   const int per = (a.blocks + kW4Waves - 1) / kW4Waves;
-  const int s0 = wave * per, s1 = min(a.blocks, s0 + per);
+  const int s0 = min(a.blocks, wave * per), s1 = min(a.blocks, s0 + per);
   constexpr uint32_t one = ones2(E());
   const u32x4 ones = {one, one, one, one};
 
   for (int64_t m0 = MODE <= kDense32 ? (int64_t)blockIdx.z * ROWS : 0; m0 < rows;
        m0 += MODE <= kDense32 ? (int64_t)gridDim.z * ROWS : ROWS) {
-    const L* xp[MT];
+    const int count = (int)min((int64_t)ROWS, rows - m0);
+    u32x4 w[PF];
+    W4Scales<E, GB, Z> sc[PF];
+    // steps past the wave's last repeat it: no branch stands between the loads
+    auto load = [&](u32x4& wr, W4Scales<E, GB, Z>& sr, int s) {
+      s = min(s, s1 - 1);
+      wr = load_codes(src, wo, s);
+      load_scales<E, GB, Z>(sr, a, src, n, s);
+    };
+    if (s0 < s1) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int64_t m = m0 + (mt * R + (i16 & 3)) * 4 + (i16 >> 2);
-      xp[mt] = nullptr;
-      if ((i16 & 3) < R && m < rows) {
-        int64_t row = first + m;
-        if (MODE == kGather) row = a.pairs[row] / a.topk;
-        xp[mt] = static_cast<const L*>(a.x) + row * a.K + q * 8;
+      for (int p = 0; p < PF; ++p) load(w[p], sc[p], s0 + p);
+    }
+    // x rows, zeros past K (the codes there may be anything)
+    for (int m = 0; m < count; ++m) {
+      const L* xr = static_cast<const L*>(a.x) + x_row<MODE>(a, first, m0 + m) * a.K;
+      for (int k = t * 8; k < a.blocks * 128; k += kW4Threads * 8) {
+        u32x4 v = {0, 0, 0, 0};
+        if (k < a.K) v = *reinterpret_cast<const u32x4*>(xr + k);
+        *reinterpret_cast<u32x4*>(s_x + m * stride + k * 2) = v;
       }
     }
-    auto load = [&](W4Step<E, GB, MT>& f, int s) {
-      f.w = *reinterpret_cast<const u32x4*>(wp + (int64_t)s * 64);
+    __syncthreads();
+    int row = (i16 & 3) % R * 4 + (i16 >> 2);
+    row = row < count ? row : 0;
+    const char* xp = s_x + row * stride + q * 16;
+    float acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = 0.f;
+    auto use = [&](u32x4& wr, W4Scales<E, GB, Z>& sr, int s) {
+      loaded(wr);
+      sr.loaded();
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
-        const int64_t at = (int64_t)min(s * GP + g, a.groups - 1) * a.N;
-        f.s[g] = sp[at];
-        f.z[g] = zp ? zp[at] : 8;
+        f32x4 tt = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < GB; ++b) {
+          const int j = g * GB + b;
+          const u32x4 x = *reinterpret_cast<const u32x4*>(xp + s * 256 + j * 64);
+          tt = mfma16(E(), x, codes8(E(), wr[j]), tt);
+          xs = mfma16(E(), x, ones, xs);
+        }
+        const float scale = sr.scale(g), off = sr.offset(g);
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = fmaf(scale, fmaf(off, xs[r], tt[r]), acc[r]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int s = s0;
+    for (; s + PF <= s1; s += PF) {
+#pragma unroll
+      for (int p = 0; p < PF; ++p) {
+        use(w[p], sc[p], s + p);
+        __builtin_amdgcn_sched_barrier(0);   // a load kept behind the use needs no other registers
+        load(w[p], sc[p], s + p + PF);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < PF; ++p)
+      if (s + p < s1) use(w[p], sc[p], s + p);
+#pragma unroll
+    for (int r = 0; r < R; ++r) s_part[wave][r][lane] = acc[r];
+    __syncthreads();
+    for (int o = t; o < R * 64; o += kW4Threads) {
+      const int l = o & 63, m = (o >> 6) * 4 + (l >> 4), col = n0 + (l & 15);
+      if (m < count && col < a.N) {
+        float v = 0.f;
+#pragma unroll
+        for (int u = 0; u < kW4Waves; ++u) v += s_part[u][o >> 6][l];
+        store_out<E, MODE>(a, first, m0 + m, col, v);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+constexpr uint32_t kNoX = 0xFE000000u;   // with any k * 2 added, past every x (below kNoX bytes)
+
+// More rows: a wave keeps MT x NT tiles of 16 rows and 16 columns over its part of
+// K, so that each x it reads (from L2) serves 16 NT columns.
+template <typename E, int GB, bool Z, int MT, int NT, W4Mode MODE>
+__global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
+  constexpr int ROWS = 16 * MT, GP = 4 / GB, PF = 2;
+  __shared__ float s_part[kW4Waves][MT][4][64];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int i16 = lane & 15, q = lane >> 4;
+  const int n0 = column_tile() * 16 * NT;
+  const int e = MODE == kGather || MODE == kScatter ? blockIdx.y : 0;
+  int64_t first = 0, rows = a.M;
+  if (MODE == kGather || MODE == kScatter) {
+    first = __builtin_amdgcn_readfirstlane(a.offsets[e]);
+    rows = __builtin_amdgcn_readfirstlane(a.offsets[e + 1]) - first;
+    if (rows <= 0) return;
+  }
+  const W4Source src = source_of<Z>(a, e, n0, 16 * NT);
+  uint32_t n[NT], wo[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    n[nt] = min(n0 + nt * 16 + i16, a.N - 1);
+    wo[nt] = (uint32_t)(nt * 16 + i16) * a.blocks * 64 + q * 16;
+  }
+  const int per = (a.blocks + kW4Waves - 1) / kW4Waves;
+  const int s0 = min(a.blocks, wave * per), s1 = min(a.blocks, s0 + per);
+  constexpr uint32_t one = ones2(E());
+  const u32x4 ones = {one, one, one, one};
+
+  for (int64_t m0 = MODE <= kDense32 ? (int64_t)blockIdx.z * ROWS : 0; m0 < rows;
+       m0 += MODE <= kDense32 ? (int64_t)gridDim.z * ROWS : ROWS) {
+    // byte offsets from the chunk's first row, or from the first token: below 2^32
+    const int64_t from = MODE == kGather ? 0 : first + m0;
+    const __amdgpu_buffer_rsrc_t xr =
+        resource(static_cast<const char*>(a.x) + from * a.K * 2,
+                 (MODE == kGather ? a.M : min((int64_t)ROWS, rows - m0)) * a.K * 2);
+    uint32_t xo[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)   // rows past the last repeat it
+      xo[mt] = (uint32_t)(x_row<MODE>(a, first, min(m0 + mt * 16 + i16, rows - 1)) - from) * a.K * 2 +
+               q * 16;
+    u32x4 w[PF][NT], x[PF][MT][4];
+    W4Scales<E, GB, Z> sc[PF][NT];
+    auto load = [&](int p, int s) {
+      s = min(s, s1 - 1);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        w[p][nt] = load_codes(src, wo[nt], s);
+        load_scales<E, GB, Z>(sc[p][nt], a, src, n[nt], s);
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int k = s * 128 + j * 32;
-          f.x[mt][j] = u32x4{0, 0, 0, 0};
-          if (xp[mt] && k + q * 8 < a.K)
-            f.x[mt][j] = *reinterpret_cast<const u32x4*>(xp[mt] + k);
+          const int k = s * 128 + j * 32;   // past K: an offset past the resource
+          x[p][mt][j] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, k + q * 8 < a.K ? xo[mt] : kNoX, k * 2, 0));
         }
     };
-    f32x4 acc[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto use = [&](const W4Step<E, GB, MT>& f) {
-#pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        f32x4 tt[MT], xs[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) tt[mt] = xs[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int b = 0; b < GB; ++b) {
-          const int j = g * GB + b;
-          const u32x4 c = codes8(E(), f.w[j]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            tt[mt] = mfma16(E(), f.x[mt][j], c, tt[mt]);
-            xs[mt] = mfma16(E(), f.x[mt][j], ones, xs[mt]);
-          }
-        }
-        const float scale = (float)f.s[g], off = -(code_base(E()) + (float)f.z[g]);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            acc[mt][r] = fmaf(scale, fmaf(off, xs[mt][r], tt[mt][r]), acc[mt][r]);
-      }
-    };
-    W4Step<E, GB, MT> ring[PF];
-#pragma unroll
-    for (int p = 0; p < PF; ++p)
-      if (s0 + p < s1) load(ring[p], s0 + p);
-    for (int s = s0; s < s1; s += PF) {
-#pragma unroll
-      for (int p = 0; p < PF; ++p)
-        if (s + p < s1) {
-          use(ring[p]);
-          if (s + p + PF < s1) load(ring[p], s + p + PF);
-        }
-    }
+    f32x4 acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int r = 0; r < R; ++r) s_part[wave][mt * R + r][lane] = acc[mt][r];
-    __syncthreads();
-    for (int o = t; o < MT * R * 64; o += kW4Threads) {
-      const int l = o & 63, tile = o >> 6;
-      const int64_t m = m0 + tile * 4 + (l >> 4);
-      const int col = n0 + (l & 15);
-      if (m < rows && col < a.N) {
-        float v = 0.f;
+      for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto use = [&](int p) {
 #pragma unroll
-        for (int w = 0; w < kW4Waves; ++w) v += s_part[w][tile][l];
-        if (MODE == kScatter) {
-          const int64_t p = a.pairs[first + m];
-          static_cast<float*>(a.out)[p * a.N + col] = v * a.weights[p];
-        } else if (MODE == kDense32) {
-          static_cast<float*>(a.out)[m * a.N + col] = v;
-        } else {
-          if (MODE == kGather) v = activate(v, a.act);
-          static_cast<L*>(a.out)[(first + m) * a.N + col] = (L)v;
+      for (int nt = 0; nt < NT; ++nt) {
+        loaded(w[p][nt]);
+        sc[p][nt].loaded();
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) loaded(x[p][mt][j]);
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        f32x4 xs[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          xs[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int b = 0; b < GB; ++b) xs[mt] = mfma16(E(), x[p][mt][g * GB + b], ones, xs[mt]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          f32x4 tt[MT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) tt[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int b = 0; b < GB; ++b) {
+            const u32x4 c = codes8(E(), w[p][nt][g * GB + b]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) tt[mt] = mfma16(E(), x[p][mt][g * GB + b], c, tt[mt]);
+          }
+          const float scale = sc[p][nt].scale(g), off = sc[p][nt].offset(g);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[mt][nt][r] = fmaf(scale, fmaf(off, xs[mt][r], tt[mt][r]), acc[mt][nt][r]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
+    };
+    if (s0 < s1) {
+#pragma unroll
+      for (int p = 0; p < PF; ++p) load(p, s0 + p);
     }
-    __syncthreads();
+    int s = s0;
+    for (; s + PF <= s1; s += PF) {
+#pragma unroll
+      for (int p = 0; p < PF; ++p) {
+        use(p);
+        __builtin_amdgcn_sched_barrier(0);
+        load(p, s + p + PF);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < PF; ++p)
+      if (s + p < s1) use(p);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s_part[wave][mt][r][lane] = acc[mt][nt][r];
+      __syncthreads();
+      for (int o = t; o < MT * 256; o += kW4Threads) {
+        const int l = o & 63, r = (o >> 6) & 3, mt = o >> 8;
+        const int64_t m = m0 + mt * 16 + (l >> 4) * 4 + r;
+        const int col = n0 + nt * 16 + (l & 15);
+        if (m < rows && col < a.N) {
+          float v = 0.f;
+#pragma unroll
+          for (int u = 0; u < kW4Waves; ++u) v += s_part[u][mt][r][l];
+          store_out<E, MODE>(a, first, m, col, v);
+        }
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -252,19 +468,30 @@ __global__ __launch_bounds__(256) void w4_pack(int64_t n_matrices, int64_t K, in
   }
 }
 
-template <typename E, int GB, W4Mode MODE>
+constexpr int64_t kFewLds = 128 << 10;   // most LDS that x may take
+
+template <typename E, int GB, bool Z, W4Mode MODE>
 void launch_rows(const W4Args& a, int64_t most, dim3 grid, hipStream_t stream) {
-#define FM_W4(MT, R, PF)                                                                    \
-  do {                                                                                      \
-    if (MODE <= kDense32)                                                                   \
-      grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, MT * R * 4), 65535);                   \
-    hipLaunchKernelGGL((w4_product<E, GB, MT, R, PF, MODE>), grid, dim3(kW4Threads), 0, stream, \
-                       a);                                                                  \
+  const int64_t stride = (int64_t)a.blocks * 256 + 16;
+#define FM_FEW(R)                                                                            \
+  do {                                                                                       \
+    if (MODE <= kDense32) grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, 4 * R), 65535);     \
+    const int64_t rows = MODE <= kDense32 ? std::min<int64_t>(a.M, 4 * R) : 4 * R;           \
+    hipLaunchKernelGGL((w4_few<E, GB, Z, R, MODE>), grid, dim3(kW4Threads), rows* stride, stream, a); \
   } while (0)
-  if (most <= 4) FM_W4(1, 1, 3);
-  else if (most <= 16) FM_W4(1, 4, 3);
-  else FM_W4(2, 4, 2);
-#undef FM_W4
+#define FM_MANY(MT, NT)                                                                      \
+  do {                                                                                       \
+    if (MODE <= kDense32) grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, 16 * MT), 65535);   \
+    grid.x = (unsigned)cdiv(a.N, 16 * NT);                                                   \
+    hipLaunchKernelGGL((w4_many<E, GB, Z, MT, NT, MODE>), grid, dim3(kW4Threads), 0, stream, a); \
+  } while (0)
+  if (most <= 4 && std::min<int64_t>(most, 4) * stride <= kFewLds) FM_FEW(1);
+  else if (most <= 8 && 8 * stride <= kFewLds) FM_FEW(2);
+  else if (most <= 16) FM_MANY(1, 2);
+  else if (most <= 32) FM_MANY(2, 2);
+  else FM_MANY(3, 2);
+#undef FM_FEW
+#undef FM_MANY
 }
 
 // most: the rows that a chunk is chosen for.
@@ -272,15 +499,21 @@ template <W4Mode MODE>
 void launch_w4(fm_dtype_t dt, int group, const W4Args& a, int64_t most, int n_local,
                hipStream_t stream) {
   const dim3 grid((unsigned)cdiv(a.N, 16), (unsigned)n_local, 1);
-  if (dt == FM_F16) {
-    if (group == 32) launch_rows<F16, 1, MODE>(a, most, grid, stream);
-    else if (group == 64) launch_rows<F16, 2, MODE>(a, most, grid, stream);
-    else launch_rows<F16, 4, MODE>(a, most, grid, stream);
-  } else {
-    if (group == 32) launch_rows<BF16, 1, MODE>(a, most, grid, stream);
-    else if (group == 64) launch_rows<BF16, 2, MODE>(a, most, grid, stream);
-    else launch_rows<BF16, 4, MODE>(a, most, grid, stream);
-  }
+#define FM_W4_ZERO(E, GB)                                           \
+  do {                                                              \
+    if (a.zeros) launch_rows<E, GB, true, MODE>(a, most, grid, stream); \
+    else launch_rows<E, GB, false, MODE>(a, most, grid, stream);    \
+  } while (0)
+#define FM_W4_GROUP(E)                       \
+  do {                                       \
+    if (group == 32) FM_W4_ZERO(E, 1);       \
+    else if (group == 64) FM_W4_ZERO(E, 2);  \
+    else FM_W4_ZERO(E, 4);                   \
+  } while (0)
+  if (dt == FM_F16) FM_W4_GROUP(F16);
+  else FM_W4_GROUP(BF16);
+#undef FM_W4_GROUP
+#undef FM_W4_ZERO
 }
 
 int64_t row_bytes(int64_t K) { return cdiv(K, 128) * 64; }
@@ -292,7 +525,8 @@ fm_status_t check_w4(fm_dtype_t dt, int64_t N, int64_t K, int group, const void*
   if (group != 32 && group != 64 && group != 128) return FM_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(packed) || !aligned16(scales)) return FM_ERR_INVALID_ARG;
   if (work && K > 0 && (!x || !packed || !scales)) return FM_ERR_INVALID_ARG;
-  if (N >= (1ll << 22) || K >= (1ll << 22)) return FM_ERR_UNSUPPORTED;
+  if (N >= (1ll << 22) || K >= (1ll << 22) || cdiv(K, group) * N >= (1ll << 30))
+    return FM_ERR_UNSUPPORTED;   // 32-bit offsets into one matrix's scales
   return FM_OK;
 }
 
@@ -352,6 +586,7 @@ extern "C" fm_status_t fm_moe_gather_gemm_w4(
   fm_status_t st = check_w4(dt, ffn, hidden, group, X, packed, scales, T > 0 && ffn > 0);
   if (st != FM_OK) return st;
   if (T > 0 && ffn > 0 && (!H || !aligned16(H))) return FM_ERR_INVALID_ARG;
+  if (T > 0 && T * hidden * 2 >= kNoX) return FM_ERR_UNSUPPORTED;   // 32-bit row offsets
   st = fm_moe_route(T, topk, expert_begin, n_local, topk_ids, sorted_pairs, expert_offsets, ws,
                     ws_bytes, stream);
   if (st != FM_OK || T == 0 || ffn == 0) return st;
@@ -363,6 +598,7 @@ extern "C" fm_status_t fm_moe_gather_gemm_w4(
   a.out = H;
   a.pairs = sorted_pairs;
   a.offsets = expert_offsets;
+  a.M = T;
   a.N = (int)ffn;
   a.K = (int)hidden;
   a.blocks = (int)cdiv(hidden, 128);
