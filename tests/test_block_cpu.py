@@ -257,4 +257,4 @@ def test_binding_refuses_tensors_it_cannot_pass():
     with pytest.raises(ValueError):
         fm.fm_norm_residual(None, None, resid=x)
     with pytest.raises(ValueError):
-        fm.fm_gemm_w4(x, x, x, torch.zeros(3, 8), 32)
+        fm.fm_gemm_w4(x, x, x, torch.zeros(3, 8), 48)

@@ -94,6 +94,10 @@ def test_pack(K, N, lead):
     (64, 16, 1024, 128, "fp16", "fp32", False),
     (131, 200, 328, 64, "bf16", "bf16", True),
     (300, 8, 3000, 128, "bf16", "fp32", False),
+    (4, 72, 12288, 128, "bf16", "fp32", True),
+    (7, 40, 6152, 32, "fp16", "fp32", False),
+    (8, 24, 16384, 64, "bf16", "fp32", True),
+    (3, 16, 65536, 128, "bf16", "fp32", False),
 ])
 def test_gemm_w4(M, N, K, group, dt, out, zeros):
     import torch
@@ -158,6 +162,12 @@ MOE = [  # T, hidden, ffn, E, nl, e0, topk, group, dt, zeros, act, closed (no to
     (40, 256, 200, 2, 2, 0, 2, 128, "bf16", True, 0),      # every token in both experts
     (200, 128, 136, 4, 3, 1, 2, 64, "bf16", False, 3),
     (2100, 64, 72, 8, 4, 0, 4, 32, "fp16", True, 0),
+    (4, 264, 4104, 4, 4, 0, 2, 128, "bf16", True, 3),      # eight pairs, long rows
+    (13, 4104, 40, 16, 16, 0, 3, 64, "bf16", False, 1),
+    (2, 16384, 72, 4, 2, 2, 2, 32, "fp16", True, 0),       # rows too long for LDS
+    (9, 72, 20480, 8, 8, 0, 1, 128, "bf16", True, 2),
+    (128, 136, 72, 64, 64, 0, 4, 64, "fp16", True, 3),     # 512 pairs: the most that one launch sorts
+    (129, 136, 72, 64, 64, 0, 4, 64, "fp16", True, 3),
 ]
 
 

@@ -489,25 +489,62 @@ def fm_probe_mfma(dtype, mfma16: bool, waves_per_simd: int, iters: int, zero: bo
 
 
 # -- around the block: router, norms, 4-bit weights --------------------------------
+#
+# A decode step makes these calls one token at a time, so what the binding costs
+# counts: each tensor is looked at once, and torch's own names are kept in _RT.
 
-def _args(fn: str, *checks):
-    """Pointers of (name, tensor or None, dtype, shape) checks; all tensors have
-    to be contiguous and on the current device, whose stream the call goes to."""
-    device = _torch().cuda.current_device()
-    out = []
-    for name, t, dtype, shape in checks:
-        if t is None:
-            out.append(None)
-            continue
-        if t.dtype is not dtype or t.shape != shape:
-            raise ValueError(f"{fn}: {name} must be {dtype} {tuple(shape)}, got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        if not t.is_cuda or t.device.index != device:
-            raise ValueError(f"{fn}: {name} must live on the current GPU")
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} must be contiguous")
-        out.append(t.data_ptr())
-    return out
+class _Runtime:
+    def __init__(self):
+        torch = _torch()
+        self.f16, self.bf16, self.f32 = torch.float16, torch.bfloat16, torch.float32
+        self.i32, self.u8 = torch.int32, torch.uint8
+        self.code = {torch.float16: FM_F16, torch.bfloat16: FM_BF16, torch.float32: FM_F32}
+        torch.cuda.current_device()   # initialises the device, or says why not
+        self.device = torch._C._cuda_getDevice
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.lib = lib()
+
+
+_RT = None
+
+
+def _rt() -> _Runtime:
+    global _RT
+    if _RT is None:
+        _RT = _Runtime()
+    return _RT
+
+
+def _arg(fn: str, name: str, t, dtype, shape, device: int):
+    """The address of a tensor that has this type and shape, is contiguous and
+    lies on `device`; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{fn}: {name} must be {dtype} {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{fn}: {name} must live on the current GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _ws_arg(fn: str, ws, device: int):
+    if ws is None:
+        return None, 0
+    return _arg(fn, "ws", ws, ws.dtype, ws.shape, device), ws.nbytes
+
+
+def _code(rt, dtype) -> int:
+    c = rt.code.get(dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return c
+
+
+def _on(rt, device: int, stream):
+    return rt.raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def _scratch(fn: str, n: int, device):
@@ -533,19 +570,22 @@ def fm_moe_gate(logits, topk_ids, topk_weights, score: int = FM_GATE_SOFTMAX,
                 counts=None, prob_sums=None, loss=None, ws=None, stream=None) -> None:
     """topk_ids, topk_weights [T, topk] from logits [T, E]; with counts [E + 1],
     prob_sums [E] and loss [1] (all or none) the expert counts and balance loss."""
-    torch = _torch()
+    fn, rt = "fm_moe_gate", _rt()
+    d = rt.device()
     T, E = logits.shape
     topk = topk_ids.shape[1]
-    i32, f32 = torch.int32, torch.float32
-    x, b, m, ids, w, c, s, l = _args(
-        "fm_moe_gate", ("logits", logits, logits.dtype, (T, E)), ("bias", bias, f32, (E,)),
-        ("token_mask", token_mask, torch.uint8, (T,)), ("topk_ids", topk_ids, i32, (T, topk)),
-        ("topk_weights", topk_weights, f32, (T, topk)), ("counts", counts, i32, (E + 1,)),
-        ("prob_sums", prob_sums, f32, (E,)), ("loss", loss, f32, (1,)))
-    wp, wn = _ws(ws)
-    _check("fm_moe_gate", lib().fm_moe_gate(_dt(logits), T, E, topk, int(score),
-                                            int(bool(renormalize)), float(scale), x, b, m, ids, w,
-                                            c, s, l, wp, wn, _stream(stream)))
+    wp, wn = _ws_arg(fn, ws, d)
+    st = rt.lib.fm_moe_gate(
+        _code(rt, logits.dtype), T, E, topk, score, 1 if renormalize else 0, scale,
+        _arg(fn, "logits", logits, logits.dtype, (T, E), d), _arg(fn, "bias", bias, rt.f32, (E,), d),
+        _arg(fn, "token_mask", token_mask, rt.u8, (T,), d),
+        _arg(fn, "topk_ids", topk_ids, rt.i32, (T, topk), d),
+        _arg(fn, "topk_weights", topk_weights, rt.f32, (T, topk), d),
+        _arg(fn, "counts", counts, rt.i32, (E + 1,), d),
+        _arg(fn, "prob_sums", prob_sums, rt.f32, (E,), d), _arg(fn, "loss", loss, rt.f32, (1,), d),
+        wp, wn, _on(rt, d, stream))
+    if st:
+        raise FluxMIError(fn, st)
 
 
 def fm_moe_gate_bwd(logits, topk_ids, d_logits, score: int = FM_GATE_SOFTMAX,
@@ -553,18 +593,38 @@ def fm_moe_gate_bwd(logits, topk_ids, d_logits, score: int = FM_GATE_SOFTMAX,
                     d_weights=None, counts=None, d_loss=None, stream=None) -> None:
     """d_logits [T, E] from d_weights [T, topk] (gradient of topk_weights) and
     d_loss [1] (gradient of the loss, with fm_moe_gate's counts)."""
-    torch = _torch()
+    fn, rt = "fm_moe_gate_bwd", _rt()
+    d = rt.device()
     T, E = logits.shape
     topk = topk_ids.shape[1]
-    i32, f32 = torch.int32, torch.float32
-    x, m, ids, dw, c, dl, dx = _args(
-        "fm_moe_gate_bwd", ("logits", logits, logits.dtype, (T, E)),
-        ("token_mask", token_mask, torch.uint8, (T,)), ("topk_ids", topk_ids, i32, (T, topk)),
-        ("d_weights", d_weights, f32, (T, topk)), ("counts", counts, i32, (E + 1,)),
-        ("d_loss", d_loss, f32, (1,)), ("d_logits", d_logits, logits.dtype, (T, E)))
-    _check("fm_moe_gate_bwd", lib().fm_moe_gate_bwd(
-        _dt(logits), T, E, topk, int(score), int(bool(renormalize)), float(scale), x, m, ids, dw,
-        c, dl, dx, _stream(stream)))
+    st = rt.lib.fm_moe_gate_bwd(
+        _code(rt, logits.dtype), T, E, topk, score, 1 if renormalize else 0, scale,
+        _arg(fn, "logits", logits, logits.dtype, (T, E), d),
+        _arg(fn, "token_mask", token_mask, rt.u8, (T,), d),
+        _arg(fn, "topk_ids", topk_ids, rt.i32, (T, topk), d),
+        _arg(fn, "d_weights", d_weights, rt.f32, (T, topk), d),
+        _arg(fn, "counts", counts, rt.i32, (E + 1,), d),
+        _arg(fn, "d_loss", d_loss, rt.f32, (1,), d),
+        _arg(fn, "d_logits", d_logits, logits.dtype, (T, E), d), _on(rt, d, stream))
+    if st:
+        raise FluxMIError(fn, st)
+
+
+def _first_dtype(*tensors):
+    for t in tensors:
+        if t is not None:
+            return t.dtype
+    return None
+
+
+def _norm_dtypes(rt, small, streams, blocks):
+    """(dt, stream_dt, block_dt) from the 16-bit operands, the residual stream's
+    tensors and the block's; where there is no 16-bit operand, from the others."""
+    sd, bd = _first_dtype(*streams), _first_dtype(*blocks)
+    dt = _first_dtype(*small)
+    if dt is None:
+        dt = next((x for x in (sd, bd) if x is not None and x is not rt.f32), rt.bf16)
+    return dt, dt if sd is None else sd, dt if bd is None else bd
 
 
 def fm_norm_residual(out, y, block=None, resid=None, w_post=None, w_pre=None, gate=None,
@@ -572,36 +632,25 @@ def fm_norm_residual(out, y, block=None, resid=None, w_post=None, w_pre=None, ga
                      stream=None) -> None:
     """out = resid + scale * gate * (norm(block) * w_post), y = norm(out) * w_pre;
     out or y may be None (not wanted), as may every operand (see fluxmi.h)."""
-    torch = _torch()
-    like = next((t for t in (block, resid) if t is not None), None)
+    fn = "fm_norm_residual"
+    like = resid if block is None else block
     if like is None or (out is None and y is None):
         raise ValueError("fm_norm_residual: block or resid, and out or y, are needed")
-    M, N = like.shape
-    sd = next((t.dtype for t in (resid, out) if t is not None), None)
-    dt = next((t.dtype for t in (y, w_pre, w_post, gate) if t is not None), None)
-    if dt is None:   # no 16-bit operand but the arrays themselves
-        dt = next((t.dtype for t in (resid, out, block)
-                   if t is not None and t.dtype != torch.float32), torch.bfloat16)
-    bd = block.dtype if block is not None else dt
-    sd = dt if sd is None else sd
-    G = gate.shape[0] if gate is not None else 0
-    f32 = torch.float32
-    b, r, wq, wp, g, o, yy, rq, rp = _args(
-        "fm_norm_residual", ("block", block, bd, (M, N)), ("resid", resid, sd, (M, N)),
-        ("w_post", w_post, dt, (N,)), ("w_pre", w_pre, dt, (N,)), ("gate", gate, dt, (G, N)),
-        ("out", out, sd, (M, N)), ("y", y, dt, (M, N)), ("rstd_post", rstd_post, f32, (M,)),
-        ("rstd_pre", rstd_pre, f32, (M,)))
-    _check("fm_norm_residual", lib().fm_norm_residual(
-        _DT(dt), _DT(sd), _DT(bd), M, N, b, r, wq, wp, g, G, float(scale), float(eps), o, yy, rq,
-        rp, _stream(stream)))
-
-
-def _DT(dtype) -> int:
-    torch = _torch()
-    try:
-        return {torch.float16: FM_F16, torch.bfloat16: FM_BF16, torch.float32: FM_F32}[dtype]
-    except KeyError:
-        raise TypeError(f"unsupported dtype {dtype}") from None
+    rt = _rt()
+    d, f32 = rt.device(), rt.f32
+    dt, sd, bd = _norm_dtypes(rt, (y, w_pre, w_post, gate), (resid, out), (block,))
+    shape = like.shape
+    M, N = shape
+    G = 0 if gate is None else gate.shape[0]
+    st = rt.lib.fm_norm_residual(
+        _code(rt, dt), _code(rt, sd), _code(rt, bd), M, N, _arg(fn, "block", block, bd, shape, d),
+        _arg(fn, "resid", resid, sd, shape, d), _arg(fn, "w_post", w_post, dt, (N,), d),
+        _arg(fn, "w_pre", w_pre, dt, (N,), d), _arg(fn, "gate", gate, dt, (G, N), d), G, scale, eps,
+        _arg(fn, "out", out, sd, shape, d), _arg(fn, "y", y, dt, shape, d),
+        _arg(fn, "rstd_post", rstd_post, f32, (M,), d), _arg(fn, "rstd_pre", rstd_pre, f32, (M,), d),
+        _on(rt, d, stream))
+    if st:
+        raise FluxMIError(fn, st)
 
 
 def fm_norm_residual_workspace_bytes(M: int, N: int, n_gates: int = 0) -> int:
@@ -621,30 +670,29 @@ def fm_norm_residual_bwd(d_resid, d_block, out=None, block=None, d_y=None, d_out
                          stream=None) -> None:
     """Gradients of fm_norm_residual; each of d_resid, d_block, d_w_post,
     d_w_pre and d_gate may be None (not wanted)."""
-    torch = _torch()
-    like = next((t for t in (d_y, d_out) if t is not None), None)
+    fn = "fm_norm_residual_bwd"
+    like = d_out if d_y is None else d_y
     if like is None:
         raise ValueError("fm_norm_residual_bwd: d_y or d_out is needed")
-    M, N = like.shape
-    f32 = torch.float32
-    dt = next((t.dtype for t in (d_y, w_pre, w_post, gate) if t is not None), None)
-    if dt is None:
-        dt = next((t.dtype for t in (d_out, d_resid, block, d_block)
-                   if t is not None and t.dtype != f32), torch.bfloat16)
-    sd = next((t.dtype for t in (d_out, out, d_resid) if t is not None), dt)
-    bd = next((t.dtype for t in (block, d_block) if t is not None), dt)
-    G = gate.shape[0] if gate is not None else 0
-    dy, do, o, b, wq, wp, g, rq, rp, dr, db, dwq, dwp, dg = _args(
-        "fm_norm_residual_bwd", ("d_y", d_y, dt, (M, N)), ("d_out", d_out, sd, (M, N)),
-        ("out", out, sd, (M, N)), ("block", block, bd, (M, N)), ("w_post", w_post, dt, (N,)),
-        ("w_pre", w_pre, dt, (N,)), ("gate", gate, dt, (G, N)), ("rstd_post", rstd_post, f32, (M,)),
-        ("rstd_pre", rstd_pre, f32, (M,)), ("d_resid", d_resid, sd, (M, N)),
-        ("d_block", d_block, bd, (M, N)), ("d_w_post", d_w_post, f32, (N,)),
-        ("d_w_pre", d_w_pre, f32, (N,)), ("d_gate", d_gate, f32, (G, N)))
-    wsp, wsn = _ws(ws)
-    _check("fm_norm_residual_bwd", lib().fm_norm_residual_bwd(
-        _DT(dt), _DT(sd), _DT(bd), M, N, dy, do, o, b, wq, wp, g, G, float(scale), rq, rp, dr, db,
-        dwq, dwp, dg, wsp, wsn, _stream(stream)))
+    rt = _rt()
+    d, f32 = rt.device(), rt.f32
+    dt, sd, bd = _norm_dtypes(rt, (d_y, w_pre, w_post, gate), (d_out, out, d_resid),
+                              (block, d_block))
+    shape = like.shape
+    M, N = shape
+    G = 0 if gate is None else gate.shape[0]
+    wp, wn = _ws_arg(fn, ws, d)
+    st = rt.lib.fm_norm_residual_bwd(
+        _code(rt, dt), _code(rt, sd), _code(rt, bd), M, N, _arg(fn, "d_y", d_y, dt, shape, d),
+        _arg(fn, "d_out", d_out, sd, shape, d), _arg(fn, "out", out, sd, shape, d),
+        _arg(fn, "block", block, bd, shape, d), _arg(fn, "w_post", w_post, dt, (N,), d),
+        _arg(fn, "w_pre", w_pre, dt, (N,), d), _arg(fn, "gate", gate, dt, (G, N), d), G, scale,
+        _arg(fn, "rstd_post", rstd_post, f32, (M,), d), _arg(fn, "rstd_pre", rstd_pre, f32, (M,), d),
+        _arg(fn, "d_resid", d_resid, sd, shape, d), _arg(fn, "d_block", d_block, bd, shape, d),
+        _arg(fn, "d_w_post", d_w_post, f32, (N,), d), _arg(fn, "d_w_pre", d_w_pre, f32, (N,), d),
+        _arg(fn, "d_gate", d_gate, f32, (G, N), d), wp, wn, _on(rt, d, stream))
+    if st:
+        raise FluxMIError(fn, st)
 
 
 def fm_w4_row_bytes(K: int) -> int:
@@ -654,38 +702,41 @@ def fm_w4_row_bytes(K: int) -> int:
 
 def fm_w4_pack(codes, packed, stream=None) -> None:
     """Codes uint8 [..., K, N] (0..15) into packed uint8 [..., N, fm_w4_row_bytes(K)]."""
-    torch = _torch()
+    fn, rt = "fm_w4_pack", _rt()
+    d = rt.device()
     lead, (K, N) = tuple(codes.shape[:-2]), codes.shape[-2:]
     n = 1
-    for d in lead:
-        n *= d
-    c, p = _args("fm_w4_pack", ("codes", codes, torch.uint8, codes.shape),
-                 ("packed", packed, torch.uint8, lead + (N, fm_w4_row_bytes(K))))
-    _check("fm_w4_pack", lib().fm_w4_pack(n, K, N, c, p, _stream(stream)))
+    for x in lead:
+        n *= x
+    st = rt.lib.fm_w4_pack(n, K, N, _arg(fn, "codes", codes, rt.u8, codes.shape, d),
+                           _arg(fn, "packed", packed, rt.u8, lead + (N, -(-K // 128) * 64), d),
+                           _on(rt, d, stream))
+    if st:
+        raise FluxMIError(fn, st)
 
 
-def _w4_args(fn, x, packed, scales, zeros, lead, K, N, group):
-    """Pointers of a 4-bit operand of `lead` [K, N] matrices."""
+def _w4_groups(fn: str, K: int, group: int) -> int:
     if group not in (32, 64, 128):
         raise ValueError(f"{fn}: group must be 32, 64 or 128")
-    u8 = _torch().uint8
-    shape = lead + (-(-K // group), N)
-    return _args(fn, ("x", x, x.dtype, x.shape),
-                 ("packed", packed, u8, lead + (N, -(-K // 128) * 64)),
-                 ("scales", scales, x.dtype, shape), ("zeros", zeros, u8, shape))
+    return -(-K // group)
 
 
 def fm_gemm_w4(A, packed, scales, C, group: int, zeros=None, stream=None) -> None:
     """C = A @ W, W [K, N] held as 4-bit codes with scales [ceil(K / group), N]
     (and zeros of that shape, 8 without them)."""
+    fn = "fm_gemm_w4"
     M, K = A.shape
     N = C.shape[1]
-    if C.shape[0] != M:
-        raise ValueError("fm_gemm_w4: shape mismatch")
-    a, w, s, z = _w4_args("fm_gemm_w4", A, packed, scales, zeros, (), K, N, group)
-    c, = _args("fm_gemm_w4", ("C", C, C.dtype, (M, N)))
-    _check("fm_gemm_w4", lib().fm_gemm_w4(_dt(A), _dt(C), M, N, K, int(group), a, w, s, z, c,
-                                          _stream(stream)))
+    shape = (_w4_groups(fn, K, group), N)
+    rt = _rt()
+    d, dt = rt.device(), A.dtype
+    st = rt.lib.fm_gemm_w4(
+        _code(rt, dt), _code(rt, C.dtype), M, N, K, group, _arg(fn, "A", A, dt, (M, K), d),
+        _arg(fn, "packed", packed, rt.u8, (N, -(-K // 128) * 64), d),
+        _arg(fn, "scales", scales, dt, shape, d), _arg(fn, "zeros", zeros, rt.u8, shape, d),
+        _arg(fn, "C", C, C.dtype, (M, N), d), _on(rt, d, stream))
+    if st:
+        raise FluxMIError(fn, st)
 
 
 def fm_moe_gather_gemm_w4(X, topk_ids, packed, scales, H, sorted_pairs, expert_offsets,
@@ -693,21 +744,27 @@ def fm_moe_gather_gemm_w4(X, topk_ids, packed, scales, H, sorted_pairs, expert_o
                           stream=None) -> None:
     """Route, then H[rows of expert e] = act(X[gathered tokens] @ W1[e]), W1
     [n_local, hidden, ffn] in 4 bits."""
-    torch = _torch()
+    fn = "fm_moe_gather_gemm_w4"
     T, hidden = X.shape
-    topk, ffn, n_local = topk_ids.shape[1], H.shape[1], packed.shape[0]
-    if H.shape[0] < T * topk or sorted_pairs.numel() < T * topk:
-        raise ValueError("fm_moe_gather_gemm_w4: H or sorted_pairs is too short")
-    x, w, s, z = _w4_args("fm_moe_gather_gemm_w4", X, packed, scales, zeros, (n_local,), hidden,
-                          ffn, group)
-    ids, h, sp, off = _args(
-        "fm_moe_gather_gemm_w4", ("topk_ids", topk_ids, torch.int32, (T, topk)),
-        ("H", H, X.dtype, H.shape), ("sorted_pairs", sorted_pairs, torch.int32, sorted_pairs.shape),
-        ("expert_offsets", expert_offsets, torch.int32, (n_local + 1,)))
-    wp, wn = _ws(ws)
-    _check("fm_moe_gather_gemm_w4", lib().fm_moe_gather_gemm_w4(
-        _dt(X), T, hidden, ffn, topk, int(expert_begin), n_local, int(group), x, ids, w, s, z, h,
-        sp, off, int(act), wp, wn, _stream(stream)))
+    topk, nl = topk_ids.shape[1], packed.shape[0]
+    rows, ffn = H.shape
+    pairs = sorted_pairs.shape
+    if rows < T * topk or len(pairs) != 1 or pairs[0] < T * topk:
+        raise ValueError(f"{fn}: H or sorted_pairs is too short")
+    shape = (nl, _w4_groups(fn, hidden, group), ffn)
+    rt = _rt()
+    d, dt = rt.device(), X.dtype
+    wp, wn = _ws_arg(fn, ws, d)
+    st = rt.lib.fm_moe_gather_gemm_w4(
+        _code(rt, dt), T, hidden, ffn, topk, expert_begin, nl, group,
+        _arg(fn, "X", X, dt, (T, hidden), d), _arg(fn, "topk_ids", topk_ids, rt.i32, (T, topk), d),
+        _arg(fn, "packed", packed, rt.u8, (nl, ffn, -(-hidden // 128) * 64), d),
+        _arg(fn, "scales", scales, dt, shape, d), _arg(fn, "zeros", zeros, rt.u8, shape, d),
+        _arg(fn, "H", H, dt, (rows, ffn), d), _arg(fn, "sorted_pairs", sorted_pairs, rt.i32, pairs, d),
+        _arg(fn, "expert_offsets", expert_offsets, rt.i32, (nl + 1,), d), act, wp, wn,
+        _on(rt, d, stream))
+    if st:
+        raise FluxMIError(fn, st)
 
 
 def fm_moe_w4_workspace_bytes(T: int, topk: int, hidden: int) -> int:
@@ -726,20 +783,27 @@ def fm_moe_gemm_scatter_w4(H, packed, scales, topk_ids, sorted_pairs, expert_off
                            add=None, stream=None) -> None:
     """out[t] = add[t] + sum_k w[t,k] * (H[row(t,k)] @ W2[e(t,k)]) over local
     pairs, W2 [n_local, ffn, hidden] in 4 bits."""
-    torch = _torch()
+    fn = "fm_moe_gemm_scatter_w4"
     T, topk = topk_weights.shape
-    hidden, ffn, n_local = out.shape[1], H.shape[1], packed.shape[0]
-    if H.shape[0] < T * topk or sorted_pairs.numel() < T * topk:
-        raise ValueError("fm_moe_gemm_scatter_w4: H or sorted_pairs is too short")
-    h, w, s, z = _w4_args("fm_moe_gemm_scatter_w4", H, packed, scales, zeros, (n_local,), ffn,
-                          hidden, group)
-    ids, sp, off, tw, ad, o = _args(
-        "fm_moe_gemm_scatter_w4", ("topk_ids", topk_ids, torch.int32, (T, topk)),
-        ("sorted_pairs", sorted_pairs, torch.int32, sorted_pairs.shape),
-        ("expert_offsets", expert_offsets, torch.int32, (n_local + 1,)),
-        ("topk_weights", topk_weights, torch.float32, (T, topk)),
-        ("add", add, torch.float32, (T, hidden)), ("out", out, torch.float32, (T, hidden)))
-    wp, wn = _ws(ws)
-    _check("fm_moe_gemm_scatter_w4", lib().fm_moe_gemm_scatter_w4(
-        _dt(H), T, hidden, ffn, topk, int(expert_begin), n_local, int(group), h, w, s, z, ids, sp,
-        off, tw, ad, o, wp, wn, _stream(stream)))
+    rows, ffn = H.shape
+    hidden, nl = out.shape[1], packed.shape[0]
+    pairs = sorted_pairs.shape
+    if rows < T * topk or len(pairs) != 1 or pairs[0] < T * topk:
+        raise ValueError(f"{fn}: H or sorted_pairs is too short")
+    shape = (nl, _w4_groups(fn, ffn, group), hidden)
+    rt = _rt()
+    d, dt, i32, f32 = rt.device(), H.dtype, rt.i32, rt.f32
+    wp, wn = _ws_arg(fn, ws, d)
+    st = rt.lib.fm_moe_gemm_scatter_w4(
+        _code(rt, dt), T, hidden, ffn, topk, expert_begin, nl, group,
+        _arg(fn, "H", H, dt, (rows, ffn), d),
+        _arg(fn, "packed", packed, rt.u8, (nl, hidden, -(-ffn // 128) * 64), d),
+        _arg(fn, "scales", scales, dt, shape, d), _arg(fn, "zeros", zeros, rt.u8, shape, d),
+        _arg(fn, "topk_ids", topk_ids, i32, (T, topk), d),
+        _arg(fn, "sorted_pairs", sorted_pairs, i32, pairs, d),
+        _arg(fn, "expert_offsets", expert_offsets, i32, (nl + 1,), d),
+        _arg(fn, "topk_weights", topk_weights, f32, (T, topk), d),
+        _arg(fn, "add", add, f32, (T, hidden), d), _arg(fn, "out", out, f32, (T, hidden), d), wp, wn,
+        _on(rt, d, stream))
+    if st:
+        raise FluxMIError(fn, st)

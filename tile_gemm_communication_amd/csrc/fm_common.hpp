@@ -81,6 +81,11 @@ constexpr int kBufStoreThrough = 17;
 // Device properties cached once per device (compute-unit count).
 int device_cu_count();
 
+// What fm_moe_route asks of its arguments (fm_moe.hip).
+fm_status_t check_route(int64_t T, int32_t topk, int32_t n_local, const int32_t* topk_ids,
+                        const int32_t* sorted_pairs, const int32_t* expert_offsets,
+                        const void* ws, size_t ws_bytes);
+
 // Translate the last HIP launch error into a status.
 inline fm_status_t launch_status() {
   return hipGetLastError() == hipSuccess ? FM_OK : FM_ERR_HIP;

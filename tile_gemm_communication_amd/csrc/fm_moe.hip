@@ -1099,6 +1099,13 @@ fm_status_t check_route_args(int64_t T, int32_t topk, int32_t n_local, const int
 }
 
 }  // namespace
+
+fm_status_t check_route(int64_t T, int32_t topk, int32_t n_local, const int32_t* topk_ids,
+                        const int32_t* sorted_pairs, const int32_t* expert_offsets,
+                        const void* ws, size_t ws_bytes) {
+  return check_route_args(T, topk, n_local, topk_ids, sorted_pairs, expert_offsets, ws, ws_bytes);
+}
+
 }  // namespace fm
 
 using namespace fm;

@@ -20,6 +20,7 @@ namespace {
 constexpr int kW4Waves = 8;
 constexpr int kW4Threads = 64 * kW4Waves;
 constexpr int kW4MaxExperts = 64;
+constexpr int64_t kFewRows = 16;   // mean rows of an expert up to which x goes through LDS
 
 __device__ __forceinline__ f32x4 mfma16(F16, u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
@@ -62,6 +63,11 @@ struct W4Args {
   int blocks;    // 128-wide blocks of K
   int groups;
   int topk, act;
+  int n_local;
+  // a route inside the product: at most kW4Threads pairs
+  const int32_t* ids;
+  int32_t *pairs_out, *offsets_out;
+  int n_pairs, e0;
 };
 
 __device__ __forceinline__ float activate(float x, int act) {
@@ -150,6 +156,72 @@ __device__ __forceinline__ void load_scales(W4Scales<E, GB, Z>& f, const W4Args&
   }
 }
 
+// A block of an expert product: blockIdx.y-th expert that has rows, those rows'
+// places [first, first + rows), or rows = 0 past the last such expert.  Experts
+// without rows get no blocks: a decode step leaves most of them empty.
+struct W4Expert {
+  int e, first, rows;
+};
+
+// From expert_offsets, by every wave on its own: lane l looks at expert l.
+__device__ __forceinline__ W4Expert find_expert(const W4Args& a) {
+  const int lane = threadIdx.x & 63;
+  int first = 0, rows = 0;
+  if (lane < a.n_local) {
+    first = a.offsets[lane];
+    rows = a.offsets[lane + 1] - first;
+  }
+  const uint64_t has = __ballot(rows > 0);
+  const uint64_t mine = __ballot(rows > 0 && __popcll(has & ((1ull << lane) - 1)) == (int)blockIdx.y);
+  if (!mine) return {0, 0, 0};
+  const int e = __ffsll((unsigned long long)mine) - 1;
+  return {e, __builtin_amdgcn_readlane(first, e), __builtin_amdgcn_readlane(rows, e)};
+}
+
+// From topk_ids, for at most one pair a thread: the stable counting sort that
+// fm_moe_route does over its workgroups, of which each block needs one expert.
+// The rows' pairs go to s_rows; the blocks of column tile 0 write sorted_pairs
+// and expert_offsets.
+__device__ __forceinline__ W4Expert route_here(const W4Args& a, int* s_rows, int* s_count,
+                                               int* s_wave) {
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int mine = -1;
+  if (t < a.n_pairs) {
+    const int e = a.ids[t] - a.e0;
+    if (e >= 0 && e < a.n_local) mine = e;
+  }
+  if (t < kW4MaxExperts) s_count[t] = 0;
+  __syncthreads();
+  if (mine >= 0) atomicAdd(&s_count[mine], 1);
+  __syncthreads();
+  const int rows_l = s_count[lane];
+  const uint64_t has = __ballot(rows_l > 0);
+  const uint64_t hit = __ballot(rows_l > 0 && __popcll(has & ((1ull << lane) - 1)) == (int)blockIdx.y);
+  W4Expert x = {0, 0, 0};
+  if (hit) {
+    x.e = __ffsll((unsigned long long)hit) - 1;
+    x.first = __builtin_amdgcn_readfirstlane(group_sum<64>(lane < x.e ? rows_l : 0));
+    x.rows = __builtin_amdgcn_readlane(rows_l, x.e);
+  }
+  const bool in = hit && mine == x.e;
+  const uint64_t match = __ballot(in);
+  if (lane == 0) s_wave[wave] = __popcll(match);
+  __syncthreads();
+  if (in) {
+    int rank = __popcll(match & ((1ull << lane) - 1));
+    for (int w = 0; w < wave; ++w) rank += s_wave[w];
+    s_rows[rank] = t;
+    if (blockIdx.x == 0) a.pairs_out[x.first + rank] = t;
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0 && t <= a.n_local) {
+    int sum = 0;
+    for (int e = 0; e < t; ++e) sum += s_count[e];
+    a.offsets_out[t] = sum;
+  }
+  __syncthreads();
+  return x;
+}
+
 template <W4Mode MODE>
 __device__ __forceinline__ int64_t x_row(const W4Args& a, int64_t first, int64_t m) {
   return MODE == kGather ? a.pairs[first + m] / a.topk : first + m;
@@ -177,26 +249,36 @@ __device__ __forceinline__ void store_out(const W4Args& a, int64_t first, int64_
 // wait for them).  Logical row 4 r + i of a chunk is operand row 4 i + r, so that
 // only accumulators r < R of a lane are in use; operand rows without a logical
 // row repeat others, and what they give is not looked at.
-constexpr int kFewAhead = 4;   // steps of 128 k in flight
+constexpr int kFewAhead = 4;    // steps of 128 k in flight
+constexpr int kTinyAhead = 6;
 
-template <typename E, int GB, bool Z, int R, W4Mode MODE>
+template <typename E, int GB, bool Z, int R, W4Mode MODE, bool ROUTE>
 __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_few(
     const W4Args a) {
   typedef typename Elem<E>::type L;
   constexpr int ROWS = 4 * R, GP = 4 / GB, PF = kFewAhead;
   __shared__ float s_part[kW4Waves][R][64];
-  extern __shared__ char s_x[];   // rows of stride bytes
+  __shared__ int s_rows[ROUTE ? kW4Threads : 1];   // the expert's pairs
+  extern __shared__ char s_x[];                    // rows of stride bytes
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int i16 = lane & 15, q = lane >> 4;
   const int n0 = column_tile() * 16;
   const int n = min(n0 + i16, a.N - 1);
-  const int e = MODE == kGather || MODE == kScatter ? blockIdx.y : 0;
+  int e = 0;
   int64_t first = 0, rows = a.M;
   if (MODE == kGather || MODE == kScatter) {
-    first = __builtin_amdgcn_readfirstlane(a.offsets[e]);
-    rows = __builtin_amdgcn_readfirstlane(a.offsets[e + 1]) - first;
-    if (rows <= 0) return;
+    W4Expert x;
+    if constexpr (ROUTE) {
+      __shared__ int s_count[kW4MaxExperts], s_wave[kW4Waves];
+      x = route_here(a, s_rows, s_count, s_wave);
+    } else {
+      x = find_expert(a);
+    }
+    if (x.rows <= 0) return;
+    e = x.e;
+    first = x.first;
+    rows = x.rows;
   }
   const int stride = a.blocks * 256 + 16;   // rows start 16 bytes apart in the banks
   const W4Source src = source_of<Z>(a, e, n0, 16);
@@ -223,7 +305,8 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
     }
     // x rows, zeros past K (the codes there may be anything)
     for (int m = 0; m < count; ++m) {
-      const L* xr = static_cast<const L*>(a.x) + x_row<MODE>(a, first, m0 + m) * a.K;
+      const int64_t from = ROUTE ? s_rows[m0 + m] / a.topk : x_row<MODE>(a, first, m0 + m);
+      const L* xr = static_cast<const L*>(a.x) + from * a.K;
       for (int k = t * 8; k < a.blocks * 128; k += kW4Threads * 8) {
         u32x4 v = {0, 0, 0, 0};
         if (k < a.K) v = *reinterpret_cast<const u32x4*>(xr + k);
@@ -297,12 +380,14 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int i16 = lane & 15, q = lane >> 4;
   const int n0 = column_tile() * 16 * NT;
-  const int e = MODE == kGather || MODE == kScatter ? blockIdx.y : 0;
+  int e = 0;
   int64_t first = 0, rows = a.M;
   if (MODE == kGather || MODE == kScatter) {
-    first = __builtin_amdgcn_readfirstlane(a.offsets[e]);
-    rows = __builtin_amdgcn_readfirstlane(a.offsets[e + 1]) - first;
-    if (rows <= 0) return;
+    const W4Expert x = find_expert(a);
+    if (x.rows <= 0) return;
+    e = x.e;
+    first = x.first;
+    rows = x.rows;
   }
   const W4Source src = source_of<Z>(a, e, n0, 16 * NT);
   uint32_t n[NT], wo[NT];
@@ -431,6 +516,142 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
   }
 }
 
+// The second layer of a single token's few pairs (at most kTinyPairs): a block
+// owns 16 columns of out and walks every local pair, its waves sharing K, so that
+// the weighted sum needs neither a second launch nor memory between.
+constexpr int kTinyPairs = 8;
+
+struct W4TinyArgs {
+  W4Args w;             // pairs, offsets: sorted_pairs, expert_offsets; ids, e0, n_pairs
+  const float* add;
+  float* out;
+  int T;
+};
+
+template <typename E, int GB, bool Z>
+__global__ __launch_bounds__(kW4Threads) void w4_scatter_tiny(const W4TinyArgs args) {
+  typedef typename Elem<E>::type L;
+  constexpr int GP = 4 / GB, PF = kTinyAhead;
+  const W4Args& a = args.w;
+  __shared__ float s_part[kW4Waves][kTinyPairs][16];
+  extern __shared__ char s_x[];   // one row of x a pair
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int i16 = lane & 15, q = lane >> 4;
+  const int n0 = column_tile() * 16;
+  const int n = min(n0 + i16, a.N - 1);
+  const int stride = a.blocks * 256 + 16;
+  // lane p: pair p's expert (-1: not here) and its row of x
+  int ex = -1, row = -1, at_l = -1;
+  const int places = a.offsets[a.n_local];
+  if (lane < a.n_pairs) {
+    ex = a.ids[lane] - a.e0;
+    if (lane < places) at_l = a.pairs[lane];
+  }
+  for (int p = 0; p < a.n_pairs; ++p) {
+    const int at = __builtin_amdgcn_readlane(at_l, p);   // place p holds pair `at`
+    if (lane == at) row = p;
+  }
+  if (ex < 0 || ex >= a.n_local || row < 0) ex = -1;
+  const uint64_t has = __ballot(ex >= 0);
+  const int units = __popcll(has);
+  // the u-th local pair's lane
+  auto pair_of = [&](int u) {
+    uint64_t m = has;
+    for (int i = 0; i < u; ++i) m &= m - 1;
+    return __ffsll((unsigned long long)m) - 1;
+  };
+  const int per = (a.blocks + kW4Waves - 1) / kW4Waves;
+  const int s0 = min(a.blocks, wave * per), s1 = min(a.blocks, s0 + per);
+  const int steps = s1 - s0, total = steps * units;
+  u32x4 w[PF];
+  W4Scales<E, GB, Z> sc[PF];
+  int lu = 0, li = 0, lp = units ? pair_of(0) : 0;   // next to load: unit, step, pair
+  W4Source src = source_of<Z>(a, units ? __builtin_amdgcn_readlane(ex, lp) : 0, n0, 16);
+  const uint32_t wo = (uint32_t)i16 * a.blocks * 64 + q * 16;
+  auto load = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
+    wr = load_codes(src, wo, s0 + li);
+    load_scales<E, GB, Z>(sr, a, src, n, s0 + li);
+    if (++li == steps && lu + 1 < units) {   // past the last step: that one again
+      li = 0;
+      lp = pair_of(++lu);
+      src = source_of<Z>(a, __builtin_amdgcn_readlane(ex, lp), n0, 16);
+    }
+    li = min(li, steps - 1);
+  };
+  if (total > 0) {
+#pragma unroll
+    for (int p = 0; p < PF; ++p) load(w[p], sc[p]);
+  }
+  for (int u = 0; u < units; ++u) {
+    const int64_t from = __builtin_amdgcn_readlane(row, pair_of(u));
+    const L* xr = static_cast<const L*>(a.x) + from * a.K;
+    for (int k = t * 8; k < a.blocks * 128; k += kW4Threads * 8) {
+      u32x4 v = {0, 0, 0, 0};
+      if (k < a.K) v = *reinterpret_cast<const u32x4*>(xr + k);
+      *reinterpret_cast<u32x4*>(s_x + u * stride + k * 2) = v;
+    }
+  }
+  __syncthreads();
+  constexpr uint32_t one = ones2(E());
+  const u32x4 ones = {one, one, one, one};
+  float acc = 0.f;
+  int cu = 0, ci = 0;   // next to use
+  auto use = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
+    loaded(wr);
+    sr.loaded();
+    const char* xp = s_x + cu * stride + q * 16 + (s0 + ci) * 256;   // every operand row the same
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      f32x4 tt = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int b = 0; b < GB; ++b) {
+        const int j = g * GB + b;
+        const u32x4 x = *reinterpret_cast<const u32x4*>(xp + j * 64);
+        tt = mfma16(E(), x, codes8(E(), wr[j]), tt);
+        xs = mfma16(E(), x, ones, xs);
+      }
+      acc = fmaf(sr.scale(g), fmaf(sr.offset(g), xs[0], tt[0]), acc);
+    }
+    if (++ci == steps) {
+      if (lane < 16) s_part[wave][cu][lane] = acc;
+      acc = 0.f;
+      ci = 0;
+      ++cu;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int i = 0;
+  for (; i + PF <= total; i += PF) {
+#pragma unroll
+    for (int p = 0; p < PF; ++p) {
+      use(w[p], sc[p]);
+      load(w[p], sc[p]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < PF; ++p)
+    if (i + p < total) use(w[p], sc[p]);
+  if (steps <= 0 && lane < 16)
+    for (int u = 0; u < units; ++u) s_part[wave][u][lane] = 0.f;
+  __syncthreads();
+  const int col = n0 + (t & 15);
+  if (t < args.T * 16 && col < a.N) {
+    const int token = t >> 4;
+    float v = args.add ? args.add[(int64_t)token * a.N + col] : 0.f;
+    for (int k = 0; k < a.topk; ++k) {
+      const int p = token * a.topk + k;
+      if (!(has >> p & 1)) continue;
+      const int u = __popcll(has & ((1ull << p) - 1));
+      float y = 0.f;
+      for (int x = 0; x < kW4Waves; ++x) y += s_part[x][u][t & 15];
+      v += y * a.weights[p];
+    }
+    args.out[(int64_t)token * a.N + col] = v;
+  }
+}
+
 // out[t] = add[t] + sum of the weighted rows of t's local pairs, in the order of k.
 __global__ __launch_bounds__(256) void w4_join(int64_t T, int n4, int topk, int e0, int n_local,
                                                const int32_t* __restrict__ ids,
@@ -473,11 +694,12 @@ constexpr int64_t kFewLds = 128 << 10;   // most LDS that x may take
 template <typename E, int GB, bool Z, W4Mode MODE>
 void launch_rows(const W4Args& a, int64_t most, dim3 grid, hipStream_t stream) {
   const int64_t stride = (int64_t)a.blocks * 256 + 16;
-#define FM_FEW(R)                                                                            \
+#define FM_FEW(R, ROUTE)                                                                     \
   do {                                                                                       \
     if (MODE <= kDense32) grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, 4 * R), 65535);     \
-    const int64_t rows = MODE <= kDense32 ? std::min<int64_t>(a.M, 4 * R) : 4 * R;           \
-    hipLaunchKernelGGL((w4_few<E, GB, Z, R, MODE>), grid, dim3(kW4Threads), rows* stride, stream, a); \
+    const int64_t rows = std::min<int64_t>(most, 4 * R);                                     \
+    hipLaunchKernelGGL((w4_few<E, GB, Z, R, MODE, ROUTE>), grid, dim3(kW4Threads),           \
+                       rows* stride, stream, a);                                             \
   } while (0)
 #define FM_MANY(MT, NT)                                                                      \
   do {                                                                                       \
@@ -485,8 +707,15 @@ void launch_rows(const W4Args& a, int64_t most, dim3 grid, hipStream_t stream) {
     grid.x = (unsigned)cdiv(a.N, 16 * NT);                                                   \
     hipLaunchKernelGGL((w4_many<E, GB, Z, MT, NT, MODE>), grid, dim3(kW4Threads), 0, stream, a); \
   } while (0)
-  if (most <= 4 && std::min<int64_t>(most, 4) * stride <= kFewLds) FM_FEW(1);
-  else if (most <= 8 && 8 * stride <= kFewLds) FM_FEW(2);
+  if constexpr (MODE == kGather) {
+    if (a.n_pairs > 0) {
+      if (most <= 4) FM_FEW(1, true);
+      else FM_FEW(2, true);
+      return;
+    }
+  }
+  if (most <= 4 && std::min<int64_t>(most, 4) * stride <= kFewLds) FM_FEW(1, false);
+  else if (most <= 8 && 8 * stride <= kFewLds) FM_FEW(2, false);
   else if (most <= 16) FM_MANY(1, 2);
   else if (most <= 32) FM_MANY(2, 2);
   else FM_MANY(3, 2);
@@ -494,26 +723,47 @@ void launch_rows(const W4Args& a, int64_t most, dim3 grid, hipStream_t stream) {
 #undef FM_MANY
 }
 
-// most: the rows that a chunk is chosen for.
+#define FM_W4_ZERO(CALL, E, GB)     \
+  do {                              \
+    if (zeros) CALL(E, GB, true);   \
+    else CALL(E, GB, false);        \
+  } while (0)
+#define FM_W4_GROUP(CALL, E)                      \
+  do {                                            \
+    if (group == 32) FM_W4_ZERO(CALL, E, 1);      \
+    else if (group == 64) FM_W4_ZERO(CALL, E, 2); \
+    else FM_W4_ZERO(CALL, E, 4);                  \
+  } while (0)
+
+// most: the rows (of an expert) that a chunk is chosen for.
 template <W4Mode MODE>
-void launch_w4(fm_dtype_t dt, int group, const W4Args& a, int64_t most, int n_local,
+void launch_w4(fm_dtype_t dt, int group, const W4Args& a, int64_t most, int64_t experts,
                hipStream_t stream) {
-  const dim3 grid((unsigned)cdiv(a.N, 16), (unsigned)n_local, 1);
-#define FM_W4_ZERO(E, GB)                                           \
-  do {                                                              \
-    if (a.zeros) launch_rows<E, GB, true, MODE>(a, most, grid, stream); \
-    else launch_rows<E, GB, false, MODE>(a, most, grid, stream);    \
-  } while (0)
-#define FM_W4_GROUP(E)                       \
-  do {                                       \
-    if (group == 32) FM_W4_ZERO(E, 1);       \
-    else if (group == 64) FM_W4_ZERO(E, 2);  \
-    else FM_W4_ZERO(E, 4);                   \
-  } while (0)
-  if (dt == FM_F16) FM_W4_GROUP(F16);
-  else FM_W4_GROUP(BF16);
+  const dim3 grid((unsigned)cdiv(a.N, 16), (unsigned)experts, 1);
+  const uint8_t* zeros = a.zeros;
+#define FM_W4_CALL(E, GB, Z) launch_rows<E, GB, Z, MODE>(a, most, grid, stream)
+  if (dt == FM_F16) FM_W4_GROUP(FM_W4_CALL, F16);
+  else FM_W4_GROUP(FM_W4_CALL, BF16);
+#undef FM_W4_CALL
+}
+
+void launch_tiny(fm_dtype_t dt, int group, const W4TinyArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)cdiv(a.w.N, 16));
+  const uint8_t* zeros = a.w.zeros;
+  const size_t lds = (size_t)a.w.n_pairs * ((size_t)a.w.blocks * 256 + 16);
+#define FM_W4_CALL(E, GB, Z) \
+  hipLaunchKernelGGL((w4_scatter_tiny<E, GB, Z>), grid, dim3(kW4Threads), lds, stream, a)
+  if (dt == FM_F16) FM_W4_GROUP(FM_W4_CALL, F16);
+  else FM_W4_GROUP(FM_W4_CALL, BF16);
+#undef FM_W4_CALL
+}
 #undef FM_W4_GROUP
 #undef FM_W4_ZERO
+
+// Rows that an expert product is chosen for: no expert can have more than the
+// pairs, and few have more than twice the mean.
+int64_t expert_rows(int64_t pairs, int n_local) {
+  return std::min(pairs, cdiv(2 * pairs, n_local));
 }
 
 int64_t row_bytes(int64_t K) { return cdiv(K, 128) * 64; }
@@ -587,8 +837,18 @@ extern "C" fm_status_t fm_moe_gather_gemm_w4(
   if (st != FM_OK) return st;
   if (T > 0 && ffn > 0 && (!H || !aligned16(H))) return FM_ERR_INVALID_ARG;
   if (T > 0 && T * hidden * 2 >= kNoX) return FM_ERR_UNSUPPORTED;   // 32-bit row offsets
-  st = fm_moe_route(T, topk, expert_begin, n_local, topk_ids, sorted_pairs, expert_offsets, ws,
-                    ws_bytes, stream);
+  // A decode step's pairs are sorted by the product's own blocks (one launch); more
+  // pairs, or rows too long for LDS, by the route's.
+  const int64_t pairs = T * topk;
+  const bool here = T > 0 && ffn > 0 && topk > 0 && T <= kW4Threads && pairs <= kW4Threads &&
+                    n_local >= 1 && n_local <= kW4MaxExperts && pairs / n_local <= kFewRows &&
+                    8 * (cdiv(hidden, 128) * 256 + 16) <= kFewLds;
+  if (here) {
+    st = check_route(T, topk, n_local, topk_ids, sorted_pairs, expert_offsets, ws, ws_bytes);
+  } else {
+    st = fm_moe_route(T, topk, expert_begin, n_local, topk_ids, sorted_pairs, expert_offsets, ws,
+                      ws_bytes, stream);
+  }
   if (st != FM_OK || T == 0 || ffn == 0) return st;
   W4Args a = {};
   a.x = X;
@@ -605,7 +865,16 @@ extern "C" fm_status_t fm_moe_gather_gemm_w4(
   a.groups = (int)cdiv(hidden, group);
   a.topk = topk;
   a.act = act;
-  launch_w4<kGather>(dt, group, a, cdiv(2 * T * topk, n_local), n_local, stream);
+  a.n_local = n_local;
+  if (here) {
+    a.ids = topk_ids;
+    a.pairs_out = sorted_pairs;
+    a.offsets_out = expert_offsets;
+    a.n_pairs = (int)pairs;
+    a.e0 = expert_begin;
+  }
+  launch_w4<kGather>(dt, group, a, here ? pairs : expert_rows(pairs, n_local),
+                     std::min<int64_t>(n_local, pairs), stream);
   return launch_status();
 }
 
@@ -643,7 +912,18 @@ extern "C" fm_status_t fm_moe_gemm_scatter_w4(
   a.blocks = (int)cdiv(ffn, 128);
   a.groups = (int)cdiv(ffn, group);
   a.topk = topk;
-  launch_w4<kScatter>(dt, group, a, cdiv(2 * T * topk, n_local), n_local, stream);
+  a.n_local = n_local;
+  const int64_t pairs = T * topk;
+  if (pairs <= kTinyPairs && pairs * (a.blocks * 256 + 16) <= kFewLds) {
+    a.ids = topk_ids;
+    a.e0 = expert_begin;
+    a.n_pairs = (int)pairs;
+    const W4TinyArgs tiny = {a, add, out, (int)T};
+    launch_tiny(dt, group, tiny, stream);
+    return launch_status();
+  }
+  launch_w4<kScatter>(dt, group, a, expert_rows(pairs, n_local),
+                      std::min<int64_t>(n_local, pairs), stream);
   const int n4 = (int)(hidden / 4);
   hipLaunchKernelGGL(w4_join, dim3((unsigned)std::min<int64_t>(cdiv(T * n4, 256), 65536)), dim3(256),
                      0, stream, T, n4, (int)topk, (int)expert_begin, (int)n_local, topk_ids,
