@@ -23,6 +23,8 @@ constexpr float kNegInf = -__builtin_inff();
 
 // exp(x) for x <= 0 (or NaN): 1 ulp of exp2 plus the argument's rounding.
 __device__ __forceinline__ float exp_neg(float x) { return __expf(x); }
+// 1 / x within 1 ulp.
+__device__ __forceinline__ float recip(float x) { return __builtin_amdgcn_rcpf(x); }
 
 // LDS traffic between the lanes of one wave: the wave's LDS operations complete
 // in order, so only the compiler has to keep them so.
@@ -34,7 +36,35 @@ __device__ __forceinline__ void wave_lds_sync() {
 // sigmoid(x) * exp(-m) with m <= 0: for shares and renormalised weights, which
 // do not change with m; m near the largest min(x, 0) keeps them from vanishing.
 __device__ __forceinline__ float sigmoid_num(float x, float m) {
-  return exp_neg(fminf(x, 0.f) - m) / (1.f + exp_neg(-fabsf(x)));
+  return exp_neg(fminf(x, 0.f) - m) * recip(1.f + exp_neg(-fabsf(x)));
+}
+
+// The numerators of a row's shares, given m (the largest x, for a sigmoid at most
+// 0), and for a sigmoid dsig = sigmoid(-x).  Unless a row's m is far below 0,
+// e = exp(-|x|) gives all of a sigmoid's terms.
+template <int V>
+__device__ __forceinline__ void share_nums(const float (&x)[V], bool sigmoid, float m, float (&p)[V],
+                                           float (&dsig)[V]) {
+  if (!sigmoid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = exp_neg(x[v] - m);
+  } else {
+    if (__any(m < -60.f)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        p[v] = sigmoid_num(x[v], m);
+        dsig[v] = sigmoid_num(-x[v], 0.f);
+      }
+    } else {
+      const float scale = recip(exp_neg(m));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float e = exp_neg(-fabsf(x[v])), r = recip(1.f + e), er = e * r;
+        p[v] = (x[v] > 0.f ? r : er) * scale;
+        dsig[v] = x[v] > 0.f ? er : r;
+      }
+    }
+  }
 }
 
 // The expert of slot v of a lane: V / 4 chunks of 4, chunk c at (c * LPR + sub) * 4.
@@ -64,6 +94,11 @@ __device__ __forceinline__ void load_row(const typename Elem<E>::type* row, int 
   }
 }
 
+struct GatePart {
+  float sum;
+  int32_t count;
+};
+
 struct GateArgs {
   const void* logits;
   const float* bias;
@@ -73,11 +108,10 @@ struct GateArgs {
   int32_t* counts;
   float* sums;
   float* loss;
-  float* part_sums;      // [blocks, E]
-  int32_t* part_counts;  // [blocks, E + 1]
+  GatePart* part;   // [blocks, E + 1]; the last of a row counts the tokens
   int64_t T;
   int E, topk;
-  int sigmoid, renorm, stats;
+  int renorm, stats;
   float scale;
 };
 
@@ -107,7 +141,7 @@ __device__ __forceinline__ void gate_finish(const GateArgs& a, int n, Get get, d
   }
 }
 
-template <typename E, int LPR, int V, bool BIAS>
+template <typename E, int LPR, int V, bool BIAS, bool SIGMOID>
 __global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
   constexpr int G = 64 / LPR;             // rows of a wave
   constexpr int RP = G * kGateWaves;      // rows of a block and pass
@@ -144,21 +178,19 @@ __global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) x[v] = kNegInf;
     }
-    if (a.stats || !a.sigmoid) {
+    if (a.stats || !SIGMOID) {
       float m = x[0];
 #pragma unroll
       for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
       m = group_max<LPR>(m);
       if (m == kNegInf) m = 0.f;          // every share becomes 0
-      if (a.sigmoid) m = fminf(m, 0.f);
-      float p[V], sum = 0.f;
+      if (SIGMOID) m = fminf(m, 0.f);
+      float p[V], dsig[V], sum = 0.f;
+      share_nums<V>(x, SIGMOID, m, p, dsig);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        p[v] = a.sigmoid ? sigmoid_num(x[v], m) : exp_neg(x[v] - m);
-        sum += p[v];
-      }
+      for (int v = 0; v < V; ++v) sum += p[v];
       sum = group_sum<LPR>(sum);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float inv = sum == 0.f ? 0.f : recip(sum);
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] += p[v] * inv;
       if (sub == 0) {
@@ -168,9 +200,13 @@ __global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
     }
     Key key[V];
     if constexpr (BIAS) {
-      if (a.sigmoid) {
+      if (SIGMOID) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = 1.0 / (1.0 + exp(-(double)x[v]));
+        for (int v = 0; v < V; ++v) {
+          const double sc = 1.0 / (1.0 + exp(-(double)x[v]));
+          key[v] = x[v] == kNegInf ? (Key)kNegInf : sc + (Key)bias[v];
+          __builtin_amdgcn_sched_barrier(0);   // one fp64 exponential at a time: else scalars spill
+        }
       } else {
         double m = (double)x[0], sum = 0;
 #pragma unroll
@@ -181,14 +217,16 @@ __global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
         for (int v = 0; v < V; ++v) {
           key[v] = exp((double)x[v] - m);
           sum += key[v];
+          __builtin_amdgcn_sched_barrier(0);
         }
         sum = group_sum<LPR>(sum);
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = sum == 0 ? 0.0 : key[v] / sum;
+        for (int v = 0; v < V; ++v) {
+          const double sc = key[v] / sum;   // sum is 0 only where every x is -inf
+          key[v] = x[v] == kNegInf ? (Key)kNegInf : sc + (Key)bias[v];
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        key[v] = x[v] == kNegInf ? (Key)kNegInf : key[v] + (Key)bias[v];
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] = x[v];
@@ -220,17 +258,19 @@ __global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
       join(std::integral_constant<int, 16>());
       join(std::integral_constant<int, 32>());
       if (best == (Key)kNegInf) at = -1;
-      const int rel = at - sub * 4;
+      const int rel = at - sub * 4;   // of no slot where at is -1 or another lane's
       float mine = kNegInf;
       bool own = false;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const bool hit = at >= 0 && rel == (v >> 2) * LPR * 4 + (v & 3);
-        mine = hit ? x[v] : mine;
-        own = own || hit;
+        const bool hit = rel == (v >> 2) * LPR * 4 + (v & 3);
+        if (BIAS) {
+          mine = hit ? x[v] : mine;
+          own = own || hit;
+        }
         key[v] = hit ? (Key)kNegInf : key[v];
       }
-      if (own) s_x[r][k] = mine;
+      if (BIAS ? own && at >= 0 : sub == 0) s_x[r][k] = BIAS ? mine : (float)best;
       if (sub == 0) s_id[r][k] = at;
     }
     wave_lds_sync();
@@ -246,13 +286,13 @@ __global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
         if (a.renorm) {
           float m = kNegInf, sum = 0.f;
           for (int j = 0; j < topk; ++j) m = s_id[q][j] >= 0 ? fmaxf(m, s_x[q][j]) : m;
-          if (a.sigmoid) m = fminf(m, 0.f);
+          if (SIGMOID) m = fminf(m, 0.f);
           for (int j = 0; j < topk; ++j)
             if (s_id[q][j] >= 0)
-              sum += a.sigmoid ? sigmoid_num(s_x[q][j], m) : exp_neg(s_x[q][j] - m);
-          w = (a.sigmoid ? sigmoid_num(xk, m) : exp_neg(xk - m)) / sum;
+              sum += SIGMOID ? sigmoid_num(s_x[q][j], m) : exp_neg(s_x[q][j] - m);
+          w = (SIGMOID ? sigmoid_num(xk, m) : exp_neg(xk - m)) * recip(sum);
         } else {
-          w = a.sigmoid ? sigmoid_num(xk, 0.f) : exp_neg(xk - s_m[q]) * s_inv[q];
+          w = SIGMOID ? sigmoid_num(xk, 0.f) : exp_neg(xk - s_m[q]) * s_inv[q];
         }
         w *= a.scale;
         if (a.stats) atomicAdd(&s_cnt[id], 1);
@@ -279,49 +319,43 @@ __global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
       cnt = s_cnt[e];
     }, s_loss);
   } else {
-    for (int e = t; e < n; e += kGateThreads) {
-      a.part_sums[(int64_t)blockIdx.x * n + e] = block_sum(e);
-    }
     for (int e = t; e <= n; e += kGateThreads)
-      a.part_counts[(int64_t)blockIdx.x * (n + 1) + e] = s_cnt[e];
+      a.part[(int64_t)blockIdx.x * (n + 1) + e] = {e < n ? block_sum(e) : 0.f, s_cnt[e]};
   }
 }
 
 // Joins the blocks' partial sums: S threads an expert, each over every S-th
 // block, then the S parts in order.
 __global__ __launch_bounds__(kGateFinishThreads) void gate_join(const GateArgs a, int blocks) {
-  __shared__ float s_sum[kGateFinishThreads];
-  __shared__ int s_cnt[kGateFinishThreads];
-  __shared__ int s_n;
+  __shared__ GatePart s_part[2 * kGateFinishThreads];
   __shared__ double s_loss[kGateFinishThreads / 64];
-  const int t = threadIdx.x, E = a.E;
-  const int S = std::max(1, kGateFinishThreads / E);
-  if (t == 0) s_n = 0;
-  __syncthreads();
-  float sum = 0.f;
-  int cnt = 0;
-  if (t < S * E) {
-    const int e = t % E;
-#pragma unroll 8
-    for (int b = t / E; b < blocks; b += S) {
-      sum += a.part_sums[(int64_t)b * E + e];
-      cnt += a.part_counts[(int64_t)b * (E + 1) + e];
+  const int t = threadIdx.x, C = a.E + 1;   // columns
+  const int S = C < kGateFinishThreads ? kGateFinishThreads / C : 1;
+  // at most two columns a thread (C is at most one more than the threads)
+  for (int i = t; i < S * C; i += kGateFinishThreads) {
+    GatePart sum = {0.f, 0};
+    const GatePart* from = a.part + i % C;
+#pragma unroll 16
+    for (int b = i / C; b < blocks; b += S) {
+      const GatePart p = from[(int64_t)b * C];
+      sum.sum += p.sum;
+      sum.count += p.count;
     }
+    s_part[i] = sum;
   }
-  s_sum[t] = sum;
-  s_cnt[t] = cnt;
-  int tokens = 0;
-  for (int b = t; b < blocks; b += kGateFinishThreads) tokens += a.part_counts[(int64_t)b * (E + 1) + E];
-  if (tokens) atomicAdd(&s_n, tokens);
   __syncthreads();
-  gate_finish(a, s_n, [&](int e, float& s, int& c) {
+  auto get = [&](int e, float& s, int& c) {
     s = 0.f;
     c = 0;
     for (int j = 0; j < S; ++j) {
-      s += s_sum[j * E + e];
-      c += s_cnt[j * E + e];
+      s += s_part[j * C + e].sum;
+      c += s_part[j * C + e].count;
     }
-  }, s_loss);
+  };
+  float none;
+  int tokens;
+  get(a.E, none, tokens);
+  gate_finish(a, tokens, get, s_loss);
 }
 
 struct GateBwdArgs {
@@ -334,7 +368,7 @@ struct GateBwdArgs {
   void* d_logits;
   int64_t T;
   int E, topk;
-  int sigmoid, renorm;
+  int renorm;
   float scale;
 };
 
@@ -343,7 +377,7 @@ struct GateBwdArgs {
 //   slots: q_k (d_k - sum q d), q = softmax of u over the chosen (renormalised);
 //          w_k d_k, less p * sum w d for a softmax score
 //   dx = du (softmax) or du * sigmoid(-x).
-template <typename E, int LPR, int V>
+template <typename E, int LPR, int V, bool SIGMOID>
 __global__ __launch_bounds__(kGateThreads) void gate_bwd(const GateBwdArgs a) {
   typedef typename Elem<E>::type L;
   constexpr int G = 64 / LPR;
@@ -351,6 +385,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_bwd(const GateBwdArgs a) {
   __shared__ float s_x[RP][kGateMaxTopk], s_d[RP][kGateMaxTopk], s_c[RP][kGateMaxTopk];
   __shared__ int s_id[RP][kGateMaxTopk];
   __shared__ float s_m[RP], s_inv[RP];
+  __shared__ __align__(16) float s_du[RP][LPR * V];   // a row's du, where the slots are added
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int sub = lane % LPR, grp = lane / LPR, r = wave * G + grp;
   const int n = a.E, topk = a.topk;
@@ -396,17 +431,17 @@ __global__ __launch_bounds__(kGateThreads) void gate_bwd(const GateBwdArgs a) {
     for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
     m = group_max<LPR>(m);
     if (m == kNegInf) m = 0.f;
-    if (a.sigmoid) m = fminf(m, 0.f);
-    float p[V], sum = 0.f, dot = 0.f;
+    if (SIGMOID) m = fminf(m, 0.f);
+    float p[V], dsig[V], sum = 0.f, dot = 0.f;
+    share_nums<V>(x, SIGMOID, m, p, dsig);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      p[v] = a.sigmoid ? sigmoid_num(x[v], m) : exp_neg(x[v] - m);
       sum += p[v];
       dot += p[v] * ae[v];
     }
     sum = group_sum<LPR>(sum);
     dot = group_sum<LPR>(dot);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : recip(sum);
     dot *= inv;
     if (a.d_weights) {
       if (sub == 0) {
@@ -423,43 +458,58 @@ __global__ __launch_bounds__(kGateThreads) void gate_bwd(const GateBwdArgs a) {
             float mw = kNegInf, sw = 0.f, dw = 0.f;
             for (int j = 0; j < topk; ++j) mw = fmaxf(mw, s_x[q][j]);
             if (mw == kNegInf) mw = 0.f;
-            if (a.sigmoid) mw = fminf(mw, 0.f);
+            if (SIGMOID) mw = fminf(mw, 0.f);
             for (int j = 0; j < topk; ++j) {
-              const float w = a.sigmoid ? sigmoid_num(s_x[q][j], mw) : exp_neg(s_x[q][j] - mw);
+              const float w = SIGMOID ? sigmoid_num(s_x[q][j], mw) : exp_neg(s_x[q][j] - mw);
               sw += w;
               dw += w * s_d[q][j];
             }
-            const float iw = sw == 0.f ? 0.f : 1.f / sw;
-            const float w = a.sigmoid ? sigmoid_num(xk, mw) : exp_neg(xk - mw);
+            const float iw = sw == 0.f ? 0.f : recip(sw);
+            const float w = SIGMOID ? sigmoid_num(xk, mw) : exp_neg(xk - mw);
             c = w * iw * (d - dw * iw);
           } else {
-            c = d * (a.sigmoid ? sigmoid_num(xk, 0.f) : exp_neg(xk - s_m[q]) * s_inv[q]);
+            c = d * (SIGMOID ? sigmoid_num(xk, 0.f) : exp_neg(xk - s_m[q]) * s_inv[q]);
           }
         }
         s_c[q][k] = c;
       }
       wave_lds_sync();
-      if (!a.sigmoid && !a.renorm)
+      if (!SIGMOID && !a.renorm)
         for (int k = 0; k < topk; ++k) dot += s_c[r][k];
     }
     float du[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) du[v] = p[v] * inv * (ae[v] - dot);
     if (a.d_weights) {
-      for (int k = 0; k < topk; ++k) {
-        const int rel = s_id[r][k] - sub * 4;
-        const float c = s_c[r][k];
+      // through LDS: the first slot of an expert adds what all slots of it give
 #pragma unroll
-        for (int v = 0; v < V; ++v) du[v] += rel == (v >> 2) * LPR * 4 + (v & 3) ? c : 0.f;
+      for (int c = 0; c < V / 4; ++c)
+        *reinterpret_cast<f32x4*>(&s_du[r][(c * LPR + sub) * 4]) =
+            f32x4{du[c * 4], du[c * 4 + 1], du[c * 4 + 2], du[c * 4 + 3]};
+      wave_lds_sync();
+      for (int i = lane; i < G * topk; i += 64) {
+        const int q = wave * G + i / topk, k = i % topk, id = s_id[q][k];
+        float add = 0.f;
+        int first = k;
+        for (int j = topk - 1; j >= 0; --j)
+          if (s_id[q][j] == id) {
+            add += s_c[q][j];
+            first = j;
+          }
+        if (id >= 0 && first == k) s_du[q][id] += add;
+      }
+      wave_lds_sync();
+#pragma unroll
+      for (int c = 0; c < V / 4; ++c) {
+        const f32x4 d = *reinterpret_cast<const f32x4*>(&s_du[r][(c * LPR + sub) * 4]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) du[c * 4 + i] = d[i];
       }
       wave_lds_sync();
     }
-    if (a.sigmoid) {
+    if (SIGMOID) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float ex = exp_neg(-fabsf(x[v]));
-        du[v] *= (x[v] > 0.f ? ex : 1.f) / (1.f + ex);
-      }
+      for (int v = 0; v < V; ++v) du[v] *= dsig[v];
     }
     if (row < a.T) {
       L* to = static_cast<L*>(a.d_logits) + row * n;
@@ -498,7 +548,7 @@ int gate_blocks(int64_t T, int E) {
 }
 
 size_t gate_ws(int64_t T, int E) {
-  return (size_t)cdiv((int64_t)gate_blocks(T, E) * (2 * E + 1) * 4, 256) * 256;
+  return (size_t)cdiv((int64_t)gate_blocks(T, E) * (E + 1) * sizeof(GatePart), 256) * 256;
 }
 
 fm_status_t check_gate(fm_dtype_t dt, int64_t T, int E, int topk, int score, int renorm,
@@ -564,25 +614,27 @@ extern "C" fm_status_t fm_moe_gate(fm_dtype_t dt, int64_t T, int32_t n_experts, 
   a.T = T;
   a.E = n_experts;
   a.topk = topk;
-  a.sigmoid = score == FM_GATE_SIGMOID;
   a.renorm = renormalize;
   a.stats = stats;
   a.scale = scale;
   int blocks = gate_blocks(T, n_experts);
   if (stats) {
-    a.part_sums = static_cast<float*>(ws);
-    a.part_counts = static_cast<int32_t*>(ws) + (int64_t)blocks * n_experts;
+    a.part = static_cast<GatePart*>(ws);
   } else {
     blocks = (int)std::min<int64_t>(cdiv(T, kGateThreads / gate_lanes(n_experts)), 4096);
   }
-#define FM_GATE_CALL(LPR, V)                                                               \
-  do {                                                                                     \
-    if (bias)                                                                              \
-      hipLaunchKernelGGL((gate_fwd<FM_E, LPR, V, true>), dim3(blocks), dim3(kGateThreads), 0, \
-                         stream, a);                                                       \
-    else                                                                                   \
-      hipLaunchKernelGGL((gate_fwd<FM_E, LPR, V, false>), dim3(blocks), dim3(kGateThreads), 0, \
-                         stream, a);                                                       \
+#define FM_GATE_FWD(LPR, V, B, S)                                                             \
+  hipLaunchKernelGGL((gate_fwd<FM_E, LPR, V, B, S>), dim3(blocks), dim3(kGateThreads), 0, stream, \
+                     a)
+#define FM_GATE_CALL(LPR, V)                              \
+  do {                                                    \
+    if (score == FM_GATE_SIGMOID) {                       \
+      if (bias) FM_GATE_FWD(LPR, V, true, true);          \
+      else FM_GATE_FWD(LPR, V, false, true);              \
+    } else {                                              \
+      if (bias) FM_GATE_FWD(LPR, V, true, false);         \
+      else FM_GATE_FWD(LPR, V, false, false);             \
+    }                                                     \
   } while (0)
   if (dt == FM_F16) {
 #define FM_E F16
@@ -598,6 +650,7 @@ extern "C" fm_status_t fm_moe_gate(fm_dtype_t dt, int64_t T, int32_t n_experts, 
 #undef FM_E
   }
 #undef FM_GATE_CALL
+#undef FM_GATE_FWD
   if (stats && blocks > 1)
     hipLaunchKernelGGL(gate_join, dim3(1), dim3(kGateFinishThreads), 0, stream, a, blocks);
   return launch_status();
@@ -630,12 +683,18 @@ extern "C" fm_status_t fm_moe_gate_bwd(fm_dtype_t dt, int64_t T, int32_t n_exper
   a.T = T;
   a.E = n_experts;
   a.topk = topk;
-  a.sigmoid = score == FM_GATE_SIGMOID;
   a.renorm = renormalize;
   a.scale = scale;
   const int blocks = (int)std::min<int64_t>(cdiv(T, kGateThreads / gate_lanes(n_experts)), 2048);
 #define FM_GATE_CALL(LPR, V)                                                                  \
-  hipLaunchKernelGGL((gate_bwd<FM_E, LPR, V>), dim3(blocks), dim3(kGateThreads), 0, stream, a)
+  do {                                                                                        \
+    if (score == FM_GATE_SIGMOID)                                                             \
+      hipLaunchKernelGGL((gate_bwd<FM_E, LPR, V, true>), dim3(blocks), dim3(kGateThreads), 0, \
+                         stream, a);                                                          \
+    else                                                                                      \
+      hipLaunchKernelGGL((gate_bwd<FM_E, LPR, V, false>), dim3(blocks), dim3(kGateThreads), 0, \
+                         stream, a);                                                          \
+  } while (0)
   if (dt == FM_F16) {
 #define FM_E F16
     FM_GATE_LANES(FM_GATE_CALL, n_experts)

@@ -17,8 +17,10 @@
 namespace fm {
 namespace {
 
-constexpr int kW4Waves = 8;
+constexpr int kW4Waves = 8;          // few rows
 constexpr int kW4Threads = 64 * kW4Waves;
+constexpr int kManyWaves = 8;            // more rows
+constexpr int kManyThreads = 64 * kManyWaves;
 constexpr int kW4MaxExperts = 64;
 constexpr int64_t kFewRows = 16;   // mean rows of an expert up to which x goes through LDS
 
@@ -31,21 +33,47 @@ __device__ __forceinline__ f32x4 mfma16(BF16, u32x4 a, u32x4 b, f32x4 c) {
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Eight codes of a word as base + code, pair i holding nibbles i and i + 4.
-__device__ __forceinline__ u32x4 codes8(BF16, uint32_t w) {
-  constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;   // 16, ulp 1/8
-  return {((w << 3) & mask) | base, ((w >> 1) & mask) | base, ((w >> 5) & mask) | base,
-          ((w >> 9) & mask) | base};
+// 16 independent 4x4x4 products: lanes 4 b + i hold row i of A and column i of B of
+// product b (four k each), and get column i of D, its rows in the four registers.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f32x4 mfma4(F16, u32x2 a, u32x2 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, a),
+                                            __builtin_bit_cast(f16x4, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ u32x4 codes8(F16, uint32_t w) {
-  constexpr uint32_t mask = 0x00F000F0u, base = 0x54005400u;   // 64, ulp 1/16
-  return {((w << 4) & mask) | base, (w & mask) | base, ((w >> 4) & mask) | base,
-          ((w >> 8) & mask) | base};
+__device__ __forceinline__ f32x4 mfma4(BF16, u32x2 a, u32x2 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, a),
+                                                __builtin_bit_cast(s16x4, b), c, 0, 0, 0);
+}
+
+// Constants that stay in registers: as literals they would keep (x & mask) | base
+// from being one instruction (v_and_or_b32 takes no literal).
+template <typename E>
+struct W4Consts {
+  uint32_t mask, base;
+  u32x4 ones;
+  __device__ __forceinline__ W4Consts() {
+    constexpr bool half = E::id == FM_F16;
+    mask = half ? 0x00F000F0u : 0x00780078u;
+    base = half ? 0x54005400u : 0x41804180u;   // 64, ulp 1/16, or 16, ulp 1/8
+    const uint32_t one = half ? 0x3C003C00u : 0x3F803F80u;
+    ones = u32x4{one, one, one, one};
+    asm volatile("" : "+s"(mask));
+    asm volatile("" : "+v"(base));
+    asm volatile("" : "+v"(ones));
+  }
+};
+
+// Eight codes of a word as base + code, pair i holding nibbles i and i + 4.
+__device__ __forceinline__ u32x4 codes8(const W4Consts<BF16>& k, uint32_t w) {
+  return {((w << 3) & k.mask) | k.base, ((w >> 1) & k.mask) | k.base,
+          ((w >> 5) & k.mask) | k.base, ((w >> 9) & k.mask) | k.base};
+}
+__device__ __forceinline__ u32x4 codes8(const W4Consts<F16>& k, uint32_t w) {
+  return {((w << 4) & k.mask) | k.base, (w & k.mask) | k.base, ((w >> 4) & k.mask) | k.base,
+          ((w >> 8) & k.mask) | k.base};
 }
 __device__ constexpr float code_base(BF16) { return 16.f; }
 __device__ constexpr float code_base(F16) { return 64.f; }
-__device__ constexpr uint32_t ones2(BF16) { return 0x3F803F80u; }
-__device__ constexpr uint32_t ones2(F16) { return 0x3C003C00u; }
 
 enum W4Mode { kDense16, kDense32, kGather, kScatter };
 
@@ -62,8 +90,10 @@ struct W4Args {
   int N, K;
   int blocks;    // 128-wide blocks of K
   int groups;
+  int some;      // 1, or 0 with K = 0: then every resource is empty and offset 0
   int topk, act;
   int n_local;
+  int tiles;     // column tiles of a block (few rows)
   // a route inside the product: at most kW4Threads pairs
   const int32_t* ids;
   int32_t *pairs_out, *offsets_out;
@@ -90,6 +120,10 @@ __device__ __forceinline__ int column_tile() {
   return x * (n >> 3) + min(x, n & 7) + (b >> 3);
 }
 
+// An offset past every x (those have fewer bytes), also with any row's and step's
+// added to it.
+constexpr uint32_t kNoX = 0xFE000000u;
+
 // Loads go through buffer resources: the lane's 32-bit offset stays as it is and
 // the step's is a scalar, so that a load costs no address registers.  An offset
 // past the resource reads 0.
@@ -113,9 +147,9 @@ __device__ __forceinline__ W4Source source_of(const W4Args& a, int e, int n0, in
           resource(Z ? a.zeros + e * scales : nullptr, Z ? scales : 0)};
 }
 
-__device__ __forceinline__ u32x4 load_codes(const W4Source& src, uint32_t lane_offset, int step) {
+__device__ __forceinline__ u32x4 load_codes(const W4Source& src, uint32_t lane_offset, int offset) {
   return __builtin_bit_cast(u32x4,
-                            __builtin_amdgcn_raw_buffer_load_b128(src.w, lane_offset, step * 64, 0));
+                            __builtin_amdgcn_raw_buffer_load_b128(src.w, lane_offset, offset, 0));
 }
 
 // A loaded value where it is first used.  Without this the optimizer moves what
@@ -144,15 +178,16 @@ struct W4Scales {
   }
 };
 
-// n: the lane's column.  Groups past the last repeat it; x is 0 there.
+// i16: the lane's column in the tile.  Groups past the last read another (x is 0
+// there), and columns past N what follows, or 0.
 template <typename E, int GB, bool Z>
-__device__ __forceinline__ void load_scales(W4Scales<E, GB, Z>& f, const W4Args& a,
-                                            const W4Source& src, uint32_t n, int step) {
+__device__ __forceinline__ void load_scales(W4Scales<E, GB, Z>& f, const W4Source& src,
+                                            uint32_t i16, int s, int s_group, int s_last) {
 #pragma unroll
   for (int g = 0; g < 4 / GB; ++g) {
-    const int row = min(step * (4 / GB) + g, a.groups - 1) * a.N;
-    f.s[g] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src.s, n * 2, row * 2, 0);
-    if constexpr (Z) f.z[g] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.z, n, row, 0);
+    const int at = min(s + g * s_group, s_last);
+    f.s[g] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src.s, i16 * 2, at, 0);
+    if constexpr (Z) f.z[g] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.z, i16, at >> 1, 0);
   }
 }
 
@@ -243,28 +278,117 @@ __device__ __forceinline__ void store_out(const W4Args& a, int64_t first, int64_
   }
 }
 
-// Few rows (chunks of 4 R): a block owns 16 columns and its 8 waves share K in
-// contiguous parts.  x lies in LDS, so that the loads in flight are weights and
-// scales alone (memory loads complete in order: an x load behind them would
-// wait for them).  Logical row 4 r + i of a chunk is operand row 4 i + r, so that
-// only accumulators r < R of a lane are in use; operand rows without a logical
-// row repeat others, and what they give is not looked at.
-constexpr int kFewAhead = 4;    // steps of 128 k in flight
-constexpr int kTinyAhead = 6;
+// x in LDS: rows of 16-bit values, behind them the fp32 sums of their octets (8
+// values), ordered [step of 128 k][q][j] so that a lane's four lie together, and
+// places of each lane for what it has not to keep.
+struct W4Stage {
+  char* base;
+  int stride, sums, sum_stride, dump;   // bytes: of a row, start, of a row, start
+};
+
+__host__ __device__ inline int64_t stage_bytes(int blocks, int64_t rows) {
+  return rows * (blocks * 256 + blocks * 64) + 64 * 20;
+}
+
+__device__ __forceinline__ W4Stage stage_at(char* base, int blocks, int rows) {
+  return {base, blocks * 256, rows * blocks * 256, blocks * 64, rows * blocks * 320};
+}
+
+// Octet `at` (bytes / 16 of the row) of row m, if `keep`.  No branch: the compiler
+// would move the load of v into it, behind loads that are to be waited for later.
+template <typename E>
+__device__ __forceinline__ void stage_octet(const W4Stage& st, int m, uint32_t octet,
+                                            const u32x4& v, bool keep) {
+  typedef typename Raw4<E>::type L4;
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t to = keep ? m * st.stride + octet * 16 : st.dump + lane * 16;
+  const uint32_t sum_to = keep ? st.sums + m * st.sum_stride + (octet >> 4) * 64 +
+                                     (octet & 3) * 16 + (octet >> 2 & 3) * 4
+                               : st.dump + 64 * 16 + lane * 4;
+  *reinterpret_cast<u32x4*>(st.base + to) = v;
+  const f32x4 lo = widen<E>(__builtin_bit_cast(L4, u32x2{v[0], v[1]}));
+  const f32x4 hi = widen<E>(__builtin_bit_cast(L4, u32x2{v[2], v[3]}));
+  const f32x4 s = lo + hi;
+  *reinterpret_cast<float*>(st.base + sum_to) = (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Few rows: lane 4 c + q loads 16 bytes of column c, the octets 8 q + 32 j.  Four
+// neighbours share a 64-byte line (in the order that a 16x16x32 instruction takes,
+// l = 16 q + c, a load touched 64 lines and the cache's one lookup a clock was what
+// bounded the kernel).  In a 4x4x4 instruction these four lanes are the columns of
+// one product; its A rows are x at the four lanes' own k, so that row q of lane q's
+// column, the diagonal, is the lane's sum, whatever the other three are.
+// Returns one step of 128 k of row r: the part of it that is the lane's.
+template <typename E, int GB, bool Z>
+__device__ __forceinline__ float few_row(const u32x4 (&c)[4], const W4Scales<E, GB, Z>& sc,
+                                         const W4Stage& st, int step, int r) {
+  const int q = threadIdx.x & 3;
+  const char* x = st.base + r * st.stride + step * 256 + q * 16;
+  const f32x4 xs = *reinterpret_cast<const f32x4*>(st.base + st.sums + r * st.sum_stride + step * 64 + q * 16);
+  float acc = 0.f;
+#pragma unroll
+  for (int g = 0; g < 4 / GB; ++g) {
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+    float sum = xs[g * GB];
+#pragma unroll
+    for (int b = 1; b < GB; ++b) sum += xs[g * GB + b];
+#pragma unroll
+    for (int b = 0; b < GB; ++b) {
+      const int j = g * GB + b;
+      const u32x4 xv = *reinterpret_cast<const u32x4*>(x + j * 64);
+      t = mfma4(E(), u32x2{xv[0], xv[1]}, u32x2{c[j][0], c[j][1]}, t);
+      t = mfma4(E(), u32x2{xv[2], xv[3]}, u32x2{c[j][2], c[j][3]}, t);
+    }
+    const float mine = q & 2 ? (q & 1 ? t[3] : t[2]) : (q & 1 ? t[1] : t[0]);
+    acc = fmaf(sc.scale(g), fmaf(sc.offset(g), sum, mine), acc);
+  }
+  return acc;
+}
+
+// The steps of a wave: one row's sum stays in a register, several rows' in the
+// lane's own places in LDS (rows at run time: a copy of the code for each row costs
+// more in registers and first-time instruction fetches).
+template <typename E, int GB, bool Z, int R>
+__device__ __forceinline__ void few_step(const W4Consts<E>& k, u32x4& w, W4Scales<E, GB, Z>& sc,
+                                         const W4Stage& st, int step, int count, float& acc,
+                                         float* rows) {
+  loaded(w);
+  sc.loaded();
+  u32x4 c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = codes8(k, w[j]);
+  if constexpr (R == 1) {
+    acc += few_row<E, GB, Z>(c, sc, st, step, 0);
+  } else {
+#pragma clang loop unroll(disable)
+    for (int r = 0; r < count; ++r) rows[r * 64] += few_row<E, GB, Z>(c, sc, st, step, r);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// A block owns up to a.tiles tiles of 16 columns and its 8 waves share K in
+// contiguous parts; a wave streams through its part of one tile after another
+// without a stop between them.  x lies in LDS, so that the loads in flight are
+// weights and scales alone (memory loads complete in order: an x load behind them
+// would wait for them).
+#ifndef FM_AHEAD
+#define FM_AHEAD 3
+#endif
+constexpr int kAhead = FM_AHEAD;   // steps of 128 k in flight
 
 template <typename E, int GB, bool Z, int R, W4Mode MODE, bool ROUTE>
 __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_few(
     const W4Args a) {
   typedef typename Elem<E>::type L;
-  constexpr int ROWS = 4 * R, GP = 4 / GB, PF = kFewAhead;
-  __shared__ float s_part[kW4Waves][R][64];
+  constexpr int PF = kAhead, XB = 3, GP = 4 / GB;
   __shared__ int s_rows[ROUTE ? kW4Threads : 1];   // the expert's pairs
-  extern __shared__ char s_x[];                    // rows of stride bytes
-  const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int i16 = lane & 15, q = lane >> 4;
-  const int n0 = column_tile() * 16;
-  const int n = min(n0 + i16, a.N - 1);
+  __shared__ float s_row[R > 1 ? kW4Waves * R * 64 : 1];
+  extern __shared__ __align__(16) char s_dyn[];    // [tiles][waves][R][16] sums, then x
+  float* s_part = reinterpret_cast<float*>(s_dyn);
+  const W4Stage st = stage_at(s_dyn + a.tiles * (kW4Waves * R * 64), a.blocks, R);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c16 = threadIdx.x >> 2 & 15, q = threadIdx.x & 3;
+  const int n0 = column_tile() * 16 * a.tiles;
   int e = 0;
   int64_t first = 0, rows = a.M;
   if (MODE == kGather || MODE == kScatter) {
@@ -280,87 +404,135 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
     first = x.first;
     rows = x.rows;
   }
-  const int stride = a.blocks * 256 + 16;   // rows start 16 bytes apart in the banks
-  const W4Source src = source_of<Z>(a, e, n0, 16);
-  const uint32_t wo = (uint32_t)i16 * a.blocks * 64 + q * 16;   // columns past N read 0
+  const W4Source src = source_of<Z>(a, e, n0, 16 * a.tiles);
+  const uint32_t wo = (uint32_t)c16 * a.blocks * 64 + q * 16;   // columns past N read 0
   const int per = (a.blocks + kW4Waves - 1) / kW4Waves;
-  const int s0 = min(a.blocks, wave * per), s1 = min(a.blocks, s0 + per);
-  constexpr uint32_t one = ones2(E());
-  const u32x4 ones = {one, one, one, one};
+  const int s0 = min(a.blocks, wave * per), steps = min(a.blocks, s0 + per) - s0;
+  const int tiles = min(a.tiles, (a.N - n0 + 15) >> 4), total = steps * tiles;
+  const W4Consts<E> consts;
 
-  for (int64_t m0 = MODE <= kDense32 ? (int64_t)blockIdx.z * ROWS : 0; m0 < rows;
-       m0 += MODE <= kDense32 ? (int64_t)gridDim.z * ROWS : ROWS) {
-    const int count = (int)min((int64_t)ROWS, rows - m0);
+  for (int64_t m0 = MODE <= kDense32 ? (int64_t)blockIdx.z * R : 0; m0 < rows;
+       m0 += MODE <= kDense32 ? (int64_t)gridDim.z * R : R) {
+    const int count = (int)min((int64_t)R, rows - m0);
+    // x rows into LDS in pieces of 16 bytes a lane, zeros past K (the codes there
+    // may be anything).  The first pieces are asked for ahead of the weights.
+    const int64_t from = MODE == kGather ? 0 : first + m0;
+    const __amdgpu_buffer_rsrc_t xr =
+        resource(static_cast<const char*>(a.x) + from * a.K * 2,
+                 (MODE == kGather ? a.M : (int64_t)count) * a.K * 2);
+    const uint32_t lane_x = threadIdx.x * 16;
+    struct Piece {
+      int m, c;   // row, and 16 * kW4Threads-byte part of it
+    };
+    auto next = [&](Piece& p) {
+      const bool wrap = (p.c + 1) * (kW4Threads * 16) >= a.blocks * 256;
+      p.c = wrap ? 0 : p.c + 1;
+      p.m += wrap ? 1 : 0;
+    };
+    auto fetch = [&](const Piece& p) {
+      int row = min(p.m, count - 1);   // rows past the last repeat it
+      if (MODE == kGather)
+        row = ROUTE ? __builtin_amdgcn_readfirstlane(s_rows[m0 + row]) / a.topk
+                    : (int)x_row<MODE>(a, first, m0 + row);
+      const bool in = lane_x + p.c * (kW4Threads * 16) < (uint32_t)a.K * 2;
+      return __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                     xr, in ? lane_x : kNoX,
+                     (uint32_t)row * a.K * 2 + p.c * (kW4Threads * 16), 0));
+    };
+    auto place = [&](const Piece& p, const u32x4& v) {
+      const uint32_t at = lane_x + p.c * (kW4Threads * 16);
+      stage_octet<E>(st, p.m, at >> 4, v, p.m < count && at < (uint32_t)a.blocks * 256);
+    };
+    u32x4 xv[XB];
+    Piece ask = {0, 0}, put = {0, 0};
+#pragma unroll
+    for (int i = 0; i < XB; ++i) {
+      xv[i] = fetch(ask);
+      next(ask);
+    }
+
     u32x4 w[PF];
     W4Scales<E, GB, Z> sc[PF];
-    // steps past the wave's last repeat it: no branch stands between the loads
-    auto load = [&](u32x4& wr, W4Scales<E, GB, Z>& sr, int s) {
-      s = min(s, s1 - 1);
-      wr = load_codes(src, wo, s);
-      load_scales<E, GB, Z>(sr, a, src, n, s);
+    // Where the wave's next step lies in the resources (bytes, scalar): its part of K
+    // of one tile after another; past the last step, anywhere inside.
+    const int w_last = steps ? ((tiles - 1) * 16 * a.blocks + s0 + steps - 1) * 64 : 0;
+    const int s_last = ((a.groups - 1) * a.N + n0 + (tiles - 1) * 16) * 2 * a.some;
+    const int s_step = a.N * (2 * GP);
+    const int w_turn = (16 * a.blocks + 1 - steps) * 64, s_turn = 32 - (steps - 1) * s_step;
+    int li = 0, lw = min(s0 * 64, w_last), ls = min((s0 * GP * a.N + n0) * 2 * a.some, s_last);
+    auto load = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
+      wr = load_codes(src, wo, lw);
+      load_scales<E, GB, Z>(sr, src, c16, ls, a.N * 2, s_last);
+      const bool turn = ++li == steps;
+      lw = min(lw + (turn ? w_turn : 64), w_last);
+      ls = min(ls + (turn ? s_turn : s_step), s_last);
+      li = turn ? 0 : li;
     };
-    if (s0 < s1) {
+    // Every load up to here is issued by all waves on one path, needed or not (none
+    // leaves its resource): behind a branch the compiler would wait for them early.
 #pragma unroll
-      for (int p = 0; p < PF; ++p) load(w[p], sc[p], s0 + p);
+    for (int p = 0; p < PF; ++p) {
+      load(w[p], sc[p]);
+      __builtin_amdgcn_sched_barrier(0);   // in the loop's order, which the waits count by
     }
-    // x rows, zeros past K (the codes there may be anything)
-    for (int m = 0; m < count; ++m) {
-      const int64_t from = ROUTE ? s_rows[m0 + m] / a.topk : x_row<MODE>(a, first, m0 + m);
-      const L* xr = static_cast<const L*>(a.x) + from * a.K;
-      for (int k = t * 8; k < a.blocks * 128; k += kW4Threads * 8) {
-        u32x4 v = {0, 0, 0, 0};
-        if (k < a.K) v = *reinterpret_cast<const u32x4*>(xr + k);
-        *reinterpret_cast<u32x4*>(s_x + m * stride + k * 2) = v;
-      }
+#pragma unroll
+    for (int i = 0; i < XB; ++i) {
+      place(put, xv[i]);
+      next(put);
     }
+    for (; put.m < count; next(put)) place(put, fetch(put));
     __syncthreads();
-    int row = (i16 & 3) % R * 4 + (i16 >> 2);
-    row = row < count ? row : 0;
-    const char* xp = s_x + row * stride + q * 16;
-    float acc[R];
+    float acc = 0.f;
+    float* mine = s_row + (R > 1 ? wave * R * 64 + (threadIdx.x & 63) : 0);
+    if constexpr (R > 1) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) acc[r] = 0.f;
-    auto use = [&](u32x4& wr, W4Scales<E, GB, Z>& sr, int s) {
-      loaded(wr);
-      sr.loaded();
+      for (int r = 0; r < R; ++r) mine[r * 64] = 0.f;
+    }
+    int step = s0, left = steps;   // of the tile in use
+    float* sum = s_part + wave * R * 16 + c16;
+    auto use = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
+      few_step<E, GB, Z, R>(consts, wr, sr, st, step, count, acc, mine);
+      ++step;
+      if (--left == 0) {
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        f32x4 tt = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int b = 0; b < GB; ++b) {
-          const int j = g * GB + b;
-          const u32x4 x = *reinterpret_cast<const u32x4*>(xp + s * 256 + j * 64);
-          tt = mfma16(E(), x, codes8(E(), wr[j]), tt);
-          xs = mfma16(E(), x, ones, xs);
+        for (int r = 0; r < R; ++r) {
+          const float v = group_sum<4>(R > 1 ? mine[r * 64] : acc);
+          if (q == 0) sum[r * 16] = v;
+          if (R > 1) mine[r * 64] = 0.f;
+          else acc = 0.f;
         }
-        const float scale = sr.scale(g), off = sr.offset(g);
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[r] = fmaf(scale, fmaf(off, xs[r], tt[r]), acc[r]);
-        __builtin_amdgcn_sched_barrier(0);
+        sum += kW4Waves * R * 16;
+        step = s0;
+        left = steps;
       }
+      __builtin_amdgcn_sched_barrier(0);   // a load kept behind the use needs no other registers
     };
-    int s = s0;
-    for (; s + PF <= s1; s += PF) {
+    // No copy of the body for the last steps: the first pass over the code waits for
+    // its instructions too.
+#pragma clang loop unroll(disable)
+    for (int i = 0; i < total; i += PF) {
 #pragma unroll
       for (int p = 0; p < PF; ++p) {
-        use(w[p], sc[p], s + p);
-        __builtin_amdgcn_sched_barrier(0);   // a load kept behind the use needs no other registers
-        load(w[p], sc[p], s + p + PF);
+        if (i + p < total) use(w[p], sc[p]);
+        load(w[p], sc[p]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-#pragma unroll
-    for (int p = 0; p < PF; ++p)
-      if (s + p < s1) use(w[p], sc[p], s + p);
-#pragma unroll
-    for (int r = 0; r < R; ++r) s_part[wave][r][lane] = acc[r];
+    // Opaque, so that what follows from it is not held in registers all along.
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    if (steps == 0)
+      for (int o = t & 63; o < tiles * R * 16; o += 64)
+        s_part[((o / (R * 16)) * kW4Waves + wave) * R * 16 + o % (R * 16)] = 0.f;
     __syncthreads();
-    for (int o = t; o < R * 64; o += kW4Threads) {
-      const int l = o & 63, m = (o >> 6) * 4 + (l >> 4), col = n0 + (l & 15);
+    for (int o = t; o < tiles * R * 16; o += kW4Threads) {
+      const int tile = o / (R * 16), m = (o >> 4) % R, col = n0 + tile * 16 + (o & 15);
       if (m < count && col < a.N) {
         float v = 0.f;
 #pragma unroll
-        for (int u = 0; u < kW4Waves; ++u) v += s_part[u][o >> 6][l];
+        for (int u = 0; u < kW4Waves; ++u)
+          v += s_part[(tile * kW4Waves + u) * R * 16 + o % (R * 16)];
         store_out<E, MODE>(a, first, m0 + m, col, v);
       }
     }
@@ -368,14 +540,12 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
   }
 }
 
-constexpr uint32_t kNoX = 0xFE000000u;   // with any k * 2 added, past every x (below kNoX bytes)
-
 // More rows: a wave keeps MT x NT tiles of 16 rows and 16 columns over its part of
 // K, so that each x it reads (from L2) serves 16 NT columns.
 template <typename E, int GB, bool Z, int MT, int NT, W4Mode MODE>
-__global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
+__global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
   constexpr int ROWS = 16 * MT, GP = 4 / GB, PF = 2;
-  __shared__ float s_part[kW4Waves][MT][4][64];
+  __shared__ float s_part[kManyWaves][MT][4][64];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int i16 = lane & 15, q = lane >> 4;
@@ -390,16 +560,12 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
     rows = x.rows;
   }
   const W4Source src = source_of<Z>(a, e, n0, 16 * NT);
-  uint32_t n[NT], wo[NT];
+  uint32_t wo[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    n[nt] = min(n0 + nt * 16 + i16, a.N - 1);
-    wo[nt] = (uint32_t)(nt * 16 + i16) * a.blocks * 64 + q * 16;
-  }
-  const int per = (a.blocks + kW4Waves - 1) / kW4Waves;
+  for (int nt = 0; nt < NT; ++nt) wo[nt] = (uint32_t)(nt * 16 + i16) * a.blocks * 64 + q * 16;
+  const int per = (a.blocks + kManyWaves - 1) / kManyWaves;
   const int s0 = min(a.blocks, wave * per), s1 = min(a.blocks, s0 + per);
-  constexpr uint32_t one = ones2(E());
-  const u32x4 ones = {one, one, one, one};
+  const W4Consts<E> consts;
 
   for (int64_t m0 = MODE <= kDense32 ? (int64_t)blockIdx.z * ROWS : 0; m0 < rows;
        m0 += MODE <= kDense32 ? (int64_t)gridDim.z * ROWS : ROWS) {
@@ -416,11 +582,12 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
     u32x4 w[PF][NT], x[PF][MT][4];
     W4Scales<E, GB, Z> sc[PF][NT];
     auto load = [&](int p, int s) {
-      s = min(s, s1 - 1);
+      s = max(min(s, s1 - 1), 0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        w[p][nt] = load_codes(src, wo[nt], s);
-        load_scales<E, GB, Z>(sc[p][nt], a, src, n[nt], s);
+        w[p][nt] = load_codes(src, wo[nt], s * 64);
+        load_scales<E, GB, Z>(sc[p][nt], src, i16, (s * GP * a.N + n0 + nt * 16) * 2 * a.some, a.N * 2,
+                              ((a.groups - 1) * a.N + n0 + nt * 16) * 2 * a.some);
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -428,7 +595,8 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
         for (int j = 0; j < 4; ++j) {
           const int k = s * 128 + j * 32;   // past K: an offset past the resource
           x[p][mt][j] = __builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, k + q * 8 < a.K ? xo[mt] : kNoX, k * 2, 0));
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                         xr, k + q * 8 < a.K ? xo[mt] : kNoX, min(k, max(a.K - 8, 0)) * 2, 0));
         }
     };
     f32x4 acc[MT][NT];
@@ -446,6 +614,7 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int j = 0; j < 4; ++j) loaded(x[p][mt][j]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
         f32x4 xs[MT];
@@ -453,8 +622,9 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
         for (int mt = 0; mt < MT; ++mt) {
           xs[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int b = 0; b < GB; ++b) xs[mt] = mfma16(E(), x[p][mt][g * GB + b], ones, xs[mt]);
+          for (int b = 0; b < GB; ++b) xs[mt] = mfma16(E(), x[p][mt][g * GB + b], consts.ones, xs[mt]);
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           f32x4 tt[MT];
@@ -462,7 +632,7 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
           for (int mt = 0; mt < MT; ++mt) tt[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int b = 0; b < GB; ++b) {
-            const u32x4 c = codes8(E(), w[p][nt][g * GB + b]);
+            const u32x4 c = codes8(consts, w[p][nt][g * GB + b]);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) tt[mt] = mfma16(E(), x[p][mt][g * GB + b], c, tt[mt]);
           }
@@ -476,23 +646,21 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
         }
       }
     };
-    if (s0 < s1) {
 #pragma unroll
-      for (int p = 0; p < PF; ++p) load(p, s0 + p);
+    for (int p = 0; p < PF; ++p) {   // on one path and in the loop's order, as in w4_few
+      load(p, s0 + p);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    int s = s0;
-    for (; s + PF <= s1; s += PF) {
+#pragma clang loop unroll(disable)
+    for (int s = s0; s < s1; s += PF) {
 #pragma unroll
       for (int p = 0; p < PF; ++p) {
-        use(p);
+        if (s + p < s1) use(p);
         __builtin_amdgcn_sched_barrier(0);
         load(p, s + p + PF);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-#pragma unroll
-    for (int p = 0; p < PF; ++p)
-      if (s + p < s1) use(p);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -500,14 +668,14 @@ __global__ __launch_bounds__(kW4Threads) void w4_many(const W4Args a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) s_part[wave][mt][r][lane] = acc[mt][nt][r];
       __syncthreads();
-      for (int o = t; o < MT * 256; o += kW4Threads) {
+      for (int o = t; o < MT * 256; o += kManyThreads) {
         const int l = o & 63, r = (o >> 6) & 3, mt = o >> 8;
         const int64_t m = m0 + mt * 16 + (l >> 4) * 4 + r;
         const int col = n0 + nt * 16 + (l & 15);
         if (m < rows && col < a.N) {
           float v = 0.f;
 #pragma unroll
-          for (int u = 0; u < kW4Waves; ++u) v += s_part[u][mt][r][l];
+          for (int u = 0; u < kManyWaves; ++u) v += s_part[u][mt][r][l];
           store_out<E, MODE>(a, first, m, col, v);
         }
       }
@@ -531,16 +699,15 @@ struct W4TinyArgs {
 template <typename E, int GB, bool Z>
 __global__ __launch_bounds__(kW4Threads) void w4_scatter_tiny(const W4TinyArgs args) {
   typedef typename Elem<E>::type L;
-  constexpr int GP = 4 / GB, PF = kTinyAhead;
+  constexpr int PF = kAhead, GP = 4 / GB;
   const W4Args& a = args.w;
   __shared__ float s_part[kW4Waves][kTinyPairs][16];
-  extern __shared__ char s_x[];   // one row of x a pair
+  extern __shared__ __align__(16) char s_dyn[];   // one row of x a pair
+  const W4Stage st = stage_at(s_dyn, a.blocks, a.n_pairs);
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int i16 = lane & 15, q = lane >> 4;
+  const int c16 = lane >> 2, q = lane & 3;
   const int n0 = column_tile() * 16;
-  const int n = min(n0 + i16, a.N - 1);
-  const int stride = a.blocks * 256 + 16;
   // lane p: pair p's expert (-1: not here) and its row of x
   int ex = -1, row = -1, at_l = -1;
   const int places = a.offsets[a.n_local];
@@ -566,22 +733,29 @@ __global__ __launch_bounds__(kW4Threads) void w4_scatter_tiny(const W4TinyArgs a
   const int steps = s1 - s0, total = steps * units;
   u32x4 w[PF];
   W4Scales<E, GB, Z> sc[PF];
-  int lu = 0, li = 0, lp = units ? pair_of(0) : 0;   // next to load: unit, step, pair
-  W4Source src = source_of<Z>(a, units ? __builtin_amdgcn_readlane(ex, lp) : 0, n0, 16);
-  const uint32_t wo = (uint32_t)i16 * a.blocks * 64 + q * 16;
+  int lu = 0;   // the pair that is loaded
+  W4Source src =
+      source_of<Z>(a, units ? __builtin_amdgcn_readlane(ex, pair_of(0)) : 0, n0, 16);
+  const uint32_t wo = (uint32_t)c16 * a.blocks * 64 + q * 16;
+  const int last = ((a.groups - 1) * a.N + n0) * 2 * a.some;
+  const int first_s = min((s0 * GP * a.N + n0) * 2 * a.some, last);
+  const int w_last = max(s0 + steps - 1, 0) * 64;
+  int lw = min(s0 * 64, w_last), ls = first_s, li = 0;
   auto load = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
-    wr = load_codes(src, wo, s0 + li);
-    load_scales<E, GB, Z>(sr, a, src, n, s0 + li);
-    if (++li == steps && lu + 1 < units) {   // past the last step: that one again
-      li = 0;
-      lp = pair_of(++lu);
-      src = source_of<Z>(a, __builtin_amdgcn_readlane(ex, lp), n0, 16);
-    }
-    li = min(li, steps - 1);
+    wr = load_codes(src, wo, lw);
+    load_scales<E, GB, Z>(sr, src, c16, ls, a.N * 2, last);
+    const bool turn = ++li == steps;
+    lw = turn ? s0 * 64 : min(lw + 64, w_last);
+    ls = turn ? first_s : min(ls + a.N * (2 * GP), last);
+    li = turn ? 0 : li;
+    lu += turn ? 1 : 0;   // past the last pair: that one again
+    const int at = pair_of(min(lu, max(units - 1, 0)));
+    src = source_of<Z>(a, units ? __builtin_amdgcn_readlane(ex, at) : 0, n0, 16);
   };
-  if (total > 0) {
 #pragma unroll
-    for (int p = 0; p < PF; ++p) load(w[p], sc[p]);
+  for (int p = 0; p < PF; ++p) {   // on one path and in the loop's order, as in w4_few
+    load(w[p], sc[p]);
+    __builtin_amdgcn_sched_barrier(0);
   }
   for (int u = 0; u < units; ++u) {
     const int64_t from = __builtin_amdgcn_readlane(row, pair_of(u));
@@ -589,50 +763,36 @@ __global__ __launch_bounds__(kW4Threads) void w4_scatter_tiny(const W4TinyArgs a
     for (int k = t * 8; k < a.blocks * 128; k += kW4Threads * 8) {
       u32x4 v = {0, 0, 0, 0};
       if (k < a.K) v = *reinterpret_cast<const u32x4*>(xr + k);
-      *reinterpret_cast<u32x4*>(s_x + u * stride + k * 2) = v;
+      stage_octet<E>(st, u, k >> 3, v, true);
     }
   }
   __syncthreads();
-  constexpr uint32_t one = ones2(E());
-  const u32x4 ones = {one, one, one, one};
+  const W4Consts<E> consts;
   float acc = 0.f;
   int cu = 0, ci = 0;   // next to use
   auto use = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
-    loaded(wr);
-    sr.loaded();
-    const char* xp = s_x + cu * stride + q * 16 + (s0 + ci) * 256;   // every operand row the same
-#pragma unroll
-    for (int g = 0; g < GP; ++g) {
-      f32x4 tt = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int b = 0; b < GB; ++b) {
-        const int j = g * GB + b;
-        const u32x4 x = *reinterpret_cast<const u32x4*>(xp + j * 64);
-        tt = mfma16(E(), x, codes8(E(), wr[j]), tt);
-        xs = mfma16(E(), x, ones, xs);
-      }
-      acc = fmaf(sr.scale(g), fmaf(sr.offset(g), xs[0], tt[0]), acc);
-    }
+    W4Stage row = st;
+    row.base += cu * st.stride;
+    row.sums += cu * (st.sum_stride - st.stride);
+    few_step<E, GB, Z, 1>(consts, wr, sr, row, s0 + ci, 1, acc, nullptr);
     if (++ci == steps) {
-      if (lane < 16) s_part[wave][cu][lane] = acc;
+      const float v = group_sum<4>(acc);
+      if (q == 0) s_part[wave][cu][c16] = v;
       acc = 0.f;
       ci = 0;
       ++cu;
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  int i = 0;
-  for (; i + PF <= total; i += PF) {
+#pragma clang loop unroll(disable)
+  for (int i = 0; i < total; i += PF) {
 #pragma unroll
     for (int p = 0; p < PF; ++p) {
-      use(w[p], sc[p]);
+      if (i + p < total) use(w[p], sc[p]);
       load(w[p], sc[p]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-#pragma unroll
-  for (int p = 0; p < PF; ++p)
-    if (i + p < total) use(w[p], sc[p]);
   if (steps <= 0 && lane < 16)
     for (int u = 0; u < units; ++u) s_part[wave][u][lane] = 0.f;
   __syncthreads();
@@ -691,31 +851,43 @@ __global__ __launch_bounds__(256) void w4_pack(int64_t n_matrices, int64_t K, in
 
 constexpr int64_t kFewLds = 128 << 10;   // most LDS that x may take
 
+// Column tiles of a block: one until there are blocks enough to fill the chip a
+// few times over, then up to 8, which spread a block's fixed costs.
+int few_tiles(int64_t blocks) {
+  static const char* env = getenv("FM_T");
+  const int64_t target = env ? atoi(env) : 1024;
+  int t = 1;
+  while (t < 8 && blocks / (2 * t) >= target) t *= 2;
+  return t;
+}
+
 template <typename E, int GB, bool Z, W4Mode MODE>
-void launch_rows(const W4Args& a, int64_t most, dim3 grid, hipStream_t stream) {
-  const int64_t stride = (int64_t)a.blocks * 256 + 16;
+void launch_rows(W4Args a, int64_t most, dim3 grid, hipStream_t stream) {
 #define FM_FEW(R, ROUTE)                                                                     \
   do {                                                                                       \
-    if (MODE <= kDense32) grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, 4 * R), 65535);     \
-    const int64_t rows = std::min<int64_t>(most, 4 * R);                                     \
+    if (MODE <= kDense32) grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, R), 65535);         \
+    a.tiles = few_tiles((int64_t)grid.x * grid.y * grid.z);                                  \
+    grid.x = (unsigned)cdiv(a.N, 16 * a.tiles);                                              \
     hipLaunchKernelGGL((w4_few<E, GB, Z, R, MODE, ROUTE>), grid, dim3(kW4Threads),           \
-                       rows* stride, stream, a);                                             \
+                       stage_bytes(a.blocks, R) + a.tiles * (kW4Waves * R * 64), stream, a); \
   } while (0)
 #define FM_MANY(MT, NT)                                                                      \
   do {                                                                                       \
     if (MODE <= kDense32) grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, 16 * MT), 65535);   \
     grid.x = (unsigned)cdiv(a.N, 16 * NT);                                                   \
-    hipLaunchKernelGGL((w4_many<E, GB, Z, MT, NT, MODE>), grid, dim3(kW4Threads), 0, stream, a); \
+    hipLaunchKernelGGL((w4_many<E, GB, Z, MT, NT, MODE>), grid, dim3(kManyThreads), 0, stream, a); \
   } while (0)
   if constexpr (MODE == kGather) {
     if (a.n_pairs > 0) {
-      if (most <= 4) FM_FEW(1, true);
-      else FM_FEW(2, true);
+      if (most == 1) FM_FEW(1, true);
+      else FM_FEW(4, true);
       return;
     }
   }
-  if (most <= 4 && std::min<int64_t>(most, 4) * stride <= kFewLds) FM_FEW(1, false);
-  else if (most <= 8 && 8 * stride <= kFewLds) FM_FEW(2, false);
+  if ((most == 1 || (most <= 8 && stage_bytes(a.blocks, 4) > kFewLds)) &&
+      stage_bytes(a.blocks, 1) <= kFewLds)
+    FM_FEW(1, false);
+  else if (most <= 8 && stage_bytes(a.blocks, 4) <= kFewLds) FM_FEW(4, false);
   else if (most <= 16) FM_MANY(1, 2);
   else if (most <= 32) FM_MANY(2, 2);
   else FM_MANY(3, 2);
@@ -750,7 +922,7 @@ void launch_w4(fm_dtype_t dt, int group, const W4Args& a, int64_t most, int64_t 
 void launch_tiny(fm_dtype_t dt, int group, const W4TinyArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)cdiv(a.w.N, 16));
   const uint8_t* zeros = a.w.zeros;
-  const size_t lds = (size_t)a.w.n_pairs * ((size_t)a.w.blocks * 256 + 16);
+  const size_t lds = stage_bytes(a.w.blocks, a.w.n_pairs);
 #define FM_W4_CALL(E, GB, Z) \
   hipLaunchKernelGGL((w4_scatter_tiny<E, GB, Z>), grid, dim3(kW4Threads), lds, stream, a)
   if (dt == FM_F16) FM_W4_GROUP(FM_W4_CALL, F16);
@@ -775,7 +947,7 @@ fm_status_t check_w4(fm_dtype_t dt, int64_t N, int64_t K, int group, const void*
   if (group != 32 && group != 64 && group != 128) return FM_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(packed) || !aligned16(scales)) return FM_ERR_INVALID_ARG;
   if (work && K > 0 && (!x || !packed || !scales)) return FM_ERR_INVALID_ARG;
-  if (N >= (1ll << 22) || K >= (1ll << 22) || cdiv(K, group) * N >= (1ll << 30))
+  if (N >= (1ll << 22) || K >= (1ll << 22) || cdiv(K, group) * N >= (1ll << 29))
     return FM_ERR_UNSUPPORTED;   // 32-bit offsets into one matrix's scales
   return FM_OK;
 }
@@ -822,6 +994,7 @@ extern "C" fm_status_t fm_gemm_w4(fm_dtype_t ab, fm_dtype_t c, int64_t M, int64_
   a.K = (int)K;
   a.blocks = (int)cdiv(K, 128);
   a.groups = (int)cdiv(K, group);
+  a.some = K > 0;
   if (c == FM_F32) launch_w4<kDense32>(ab, group, a, M, 1, stream);
   else launch_w4<kDense16>(ab, group, a, M, 1, stream);
   return launch_status();
@@ -842,7 +1015,7 @@ extern "C" fm_status_t fm_moe_gather_gemm_w4(
   const int64_t pairs = T * topk;
   const bool here = T > 0 && ffn > 0 && topk > 0 && T <= kW4Threads && pairs <= kW4Threads &&
                     n_local >= 1 && n_local <= kW4MaxExperts && pairs / n_local <= kFewRows &&
-                    8 * (cdiv(hidden, 128) * 256 + 16) <= kFewLds;
+                    hidden <= 4 * kFewLds && stage_bytes((int)cdiv(hidden, 128), 4) <= kFewLds;
   if (here) {
     st = check_route(T, topk, n_local, topk_ids, sorted_pairs, expert_offsets, ws, ws_bytes);
   } else {
@@ -863,6 +1036,7 @@ extern "C" fm_status_t fm_moe_gather_gemm_w4(
   a.K = (int)hidden;
   a.blocks = (int)cdiv(hidden, 128);
   a.groups = (int)cdiv(hidden, group);
+  a.some = hidden > 0;
   a.topk = topk;
   a.act = act;
   a.n_local = n_local;
@@ -911,10 +1085,11 @@ extern "C" fm_status_t fm_moe_gemm_scatter_w4(
   a.K = (int)ffn;
   a.blocks = (int)cdiv(ffn, 128);
   a.groups = (int)cdiv(ffn, group);
+  a.some = ffn > 0;
   a.topk = topk;
   a.n_local = n_local;
   const int64_t pairs = T * topk;
-  if (pairs <= kTinyPairs && pairs * (a.blocks * 256 + 16) <= kFewLds) {
+  if (pairs <= kTinyPairs && stage_bytes(a.blocks, pairs) <= kFewLds) {
     a.ids = topk_ids;
     a.e0 = expert_begin;
     a.n_pairs = (int)pairs;
