@@ -26,13 +26,6 @@ __device__ __forceinline__ float exp_neg(float x) { return __expf(x); }
 // 1 / x within 1 ulp.
 __device__ __forceinline__ float recip(float x) { return __builtin_amdgcn_rcpf(x); }
 
-// LDS traffic between the lanes of one wave: the wave's LDS operations complete
-// in order, so only the compiler has to keep them so.
-__device__ __forceinline__ void wave_lds_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // sigmoid(x) * exp(-m) with m <= 0: for shares and renormalised weights, which
 // do not change with m; m near the largest min(x, 0) keeps them from vanishing.
 __device__ __forceinline__ float sigmoid_num(float x, float m) {

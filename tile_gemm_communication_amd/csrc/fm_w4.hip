@@ -278,53 +278,62 @@ __device__ __forceinline__ void store_out(const W4Args& a, int64_t first, int64_
   }
 }
 
-// x in LDS: rows of 16-bit values, behind them the fp32 sums of their octets (8
-// values), ordered [step of 128 k][q][j] so that a lane's four lie together, and
-// places of each lane for what it has not to keep.
+// x in LDS: rows of 16-bit values, 16 bytes apart in the banks, behind them fp32
+// sums of x, and places of each lane for what it has not to keep.  For one row the
+// sums are those of octets (8 values), ordered [step of 128 k][q][j] so that a
+// lane's four lie together; for several rows those of 32 values, in order.
 struct W4Stage {
   char* base;
   int stride, sums, sum_stride, dump;   // bytes: of a row, start, of a row, start
 };
 
 __host__ __device__ inline int64_t stage_bytes(int blocks, int64_t rows) {
-  return rows * (blocks * 256 + blocks * 64) + 64 * 20;
+  return rows * (blocks * 320 + 16) + 64 * 20;
 }
 
 __device__ __forceinline__ W4Stage stage_at(char* base, int blocks, int rows) {
-  return {base, blocks * 256, rows * blocks * 256, blocks * 64, rows * blocks * 320};
+  return {base, blocks * 256 + 16, rows * (blocks * 256 + 16), blocks * 64,
+          rows * (blocks * 320 + 16)};
 }
 
 // Octet `at` (bytes / 16 of the row) of row m, if `keep`.  No branch: the compiler
 // would move the load of v into it, behind loads that are to be waited for later.
-template <typename E>
+template <typename E, bool ONE>
 __device__ __forceinline__ void stage_octet(const W4Stage& st, int m, uint32_t octet,
                                             const u32x4& v, bool keep) {
   typedef typename Raw4<E>::type L4;
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t to = keep ? m * st.stride + octet * 16 : st.dump + lane * 16;
-  const uint32_t sum_to = keep ? st.sums + m * st.sum_stride + (octet >> 4) * 64 +
-                                     (octet & 3) * 16 + (octet >> 2 & 3) * 4
-                               : st.dump + 64 * 16 + lane * 4;
+  const uint32_t in_row = ONE ? (octet >> 4) * 64 + (octet & 3) * 16 + (octet >> 2 & 3) * 4
+                              : (octet >> 2) * 4;
+  const uint32_t sum_to = keep && (ONE || (octet & 3) == 0) ? st.sums + m * st.sum_stride + in_row
+                                                            : st.dump + 64 * 16 + lane * 4;
   *reinterpret_cast<u32x4*>(st.base + to) = v;
   const f32x4 lo = widen<E>(__builtin_bit_cast(L4, u32x2{v[0], v[1]}));
   const f32x4 hi = widen<E>(__builtin_bit_cast(L4, u32x2{v[2], v[3]}));
   const f32x4 s = lo + hi;
-  *reinterpret_cast<float*>(st.base + sum_to) = (s[0] + s[1]) + (s[2] + s[3]);
+  float sum = (s[0] + s[1]) + (s[2] + s[3]);
+  if (!ONE) sum = group_sum<4>(sum);
+  *reinterpret_cast<float*>(st.base + sum_to) = sum;
 }
 
-// Few rows: lane 4 c + q loads 16 bytes of column c, the octets 8 q + 32 j.  Four
-// neighbours share a 64-byte line (in the order that a 16x16x32 instruction takes,
-// l = 16 q + c, a load touched 64 lines and the cache's one lookup a clock was what
-// bounded the kernel).  In a 4x4x4 instruction these four lanes are the columns of
-// one product; its A rows are x at the four lanes' own k, so that row q of lane q's
-// column, the diagonal, is the lane's sum, whatever the other three are.
-// Returns one step of 128 k of row r: the part of it that is the lane's.
+// A tile's weights are loaded with lane 4 c + q on the 16 bytes of column c that
+// hold the octets 8 q + 32 j: four neighbours share a 64-byte line.  (In the order
+// of a 16x16x32 instruction's operand, l = 16 q + c, a load touched 64 lines, and the
+// cache's one lookup a clock was what bounded the kernel.)
+
+// One row, one step of 128 k: in a 4x4x4 instruction the four lanes of a column are
+// the columns of one product; its A rows are x at the four lanes' own k, so that the
+// diagonal, row q of lane q's column, is the lane's part, whatever the others are.
 template <typename E, int GB, bool Z>
-__device__ __forceinline__ float few_row(const u32x4 (&c)[4], const W4Scales<E, GB, Z>& sc,
-                                         const W4Stage& st, int step, int r) {
+__device__ __forceinline__ float one_row_step(const W4Consts<E>& k, u32x4& w,
+                                              W4Scales<E, GB, Z>& sc, const W4Stage& st,
+                                              int step) {
   const int q = threadIdx.x & 3;
-  const char* x = st.base + r * st.stride + step * 256 + q * 16;
-  const f32x4 xs = *reinterpret_cast<const f32x4*>(st.base + st.sums + r * st.sum_stride + step * 64 + q * 16);
+  loaded(w);
+  sc.loaded();
+  const char* x = st.base + step * 256 + q * 16;
+  const f32x4 xs = *reinterpret_cast<const f32x4*>(st.base + st.sums + step * 64 + q * 16);
   float acc = 0.f;
 #pragma unroll
   for (int g = 0; g < 4 / GB; ++g) {
@@ -335,35 +344,58 @@ __device__ __forceinline__ float few_row(const u32x4 (&c)[4], const W4Scales<E, 
 #pragma unroll
     for (int b = 0; b < GB; ++b) {
       const int j = g * GB + b;
+      const u32x4 c = codes8(k, w[j]);
       const u32x4 xv = *reinterpret_cast<const u32x4*>(x + j * 64);
-      t = mfma4(E(), u32x2{xv[0], xv[1]}, u32x2{c[j][0], c[j][1]}, t);
-      t = mfma4(E(), u32x2{xv[2], xv[3]}, u32x2{c[j][2], c[j][3]}, t);
+      t = mfma4(E(), u32x2{xv[0], xv[1]}, u32x2{c[0], c[1]}, t);
+      t = mfma4(E(), u32x2{xv[2], xv[3]}, u32x2{c[2], c[3]}, t);
     }
     const float mine = q & 2 ? (q & 1 ? t[3] : t[2]) : (q & 1 ? t[1] : t[0]);
     acc = fmaf(sc.scale(g), fmaf(sc.offset(g), sum, mine), acc);
   }
+  __builtin_amdgcn_sched_barrier(0);
   return acc;
 }
 
-// The steps of a wave: one row's sum stays in a register, several rows' in the
-// lane's own places in LDS (rows at run time: a copy of the code for each row costs
-// more in registers and first-time instruction fetches).
-template <typename E, int GB, bool Z, int R>
-__device__ __forceinline__ void few_step(const W4Consts<E>& k, u32x4& w, W4Scales<E, GB, Z>& sc,
-                                         const W4Stage& st, int step, int count, float& acc,
-                                         float* rows) {
+// From the order of the load into the operand's, through 1 KiB of LDS of the wave's
+// own.  Slot 4 c + (q + c / 4) % 4 keeps both sides free of bank conflicts.
+__device__ __forceinline__ u32x4 to_operand(const u32x4& w, char* own) {
+  const int l = threadIdx.x & 63, c = l >> 2, q = l & 3, n = l & 15, k = l >> 4;
+  *reinterpret_cast<u32x4*>(own + (4 * c + ((q + (c >> 2)) & 3)) * 16) = w;
+  wave_lds_sync();
+  const u32x4 v = *reinterpret_cast<const u32x4*>(own + (4 * n + ((k + (n >> 2)) & 3)) * 16);
+  wave_lds_sync();
+  return v;
+}
+
+// Up to four rows, one step: logical row i is operand row 4 i, so that only
+// accumulator 0 of a lane, row lane / 16, is in use; the other operand rows repeat
+// these, and what they give is not looked at.
+template <typename E, int GB, bool Z>
+__device__ __forceinline__ float four_row_step(const W4Consts<E>& k, u32x4& w,
+                                               W4Scales<E, GB, Z>& sc, const W4Stage& st, int step,
+                                               int x_row, int sum_row, char* own) {
   loaded(w);
+  const u32x4 v = to_operand(w, own);
   sc.loaded();
-  u32x4 c[4];
+  const char* x = st.base + x_row * st.stride + step * 256 + (threadIdx.x >> 4 & 3) * 16;
+  const f32x4 xs =
+      *reinterpret_cast<const f32x4*>(st.base + st.sums + sum_row * st.sum_stride + step * 16);
+  float acc = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = codes8(k, w[j]);
-  if constexpr (R == 1) {
-    acc += few_row<E, GB, Z>(c, sc, st, step, 0);
-  } else {
-#pragma clang loop unroll(disable)
-    for (int r = 0; r < count; ++r) rows[r * 64] += few_row<E, GB, Z>(c, sc, st, step, r);
+  for (int g = 0; g < 4 / GB; ++g) {
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+    float sum = xs[g * GB];
+#pragma unroll
+    for (int b = 1; b < GB; ++b) sum += xs[g * GB + b];
+#pragma unroll
+    for (int b = 0; b < GB; ++b) {
+      const int j = g * GB + b;
+      t = mfma16(E(), *reinterpret_cast<const u32x4*>(x + j * 64), codes8(k, v[j]), t);
+    }
+    acc = fmaf(sc.scale(g), fmaf(sc.offset(g), sum, t[0]), acc);
   }
   __builtin_amdgcn_sched_barrier(0);
+  return acc;
 }
 
 // A block owns up to a.tiles tiles of 16 columns and its 8 waves share K in
@@ -371,10 +403,7 @@ __device__ __forceinline__ void few_step(const W4Consts<E>& k, u32x4& w, W4Scale
 // without a stop between them.  x lies in LDS, so that the loads in flight are
 // weights and scales alone (memory loads complete in order: an x load behind them
 // would wait for them).
-#ifndef FM_AHEAD
-#define FM_AHEAD 3
-#endif
-constexpr int kAhead = FM_AHEAD;   // steps of 128 k in flight
+constexpr int kAhead = 2;   // steps of 128 k in flight; 3 and 4 measured no better, 6 worse
 
 template <typename E, int GB, bool Z, int R, W4Mode MODE, bool ROUTE>
 __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_few(
@@ -382,12 +411,13 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
   typedef typename Elem<E>::type L;
   constexpr int PF = kAhead, XB = 3, GP = 4 / GB;
   __shared__ int s_rows[ROUTE ? kW4Threads : 1];   // the expert's pairs
-  __shared__ float s_row[R > 1 ? kW4Waves * R * 64 : 1];
+  __shared__ __align__(16) char s_own[R > 1 ? kW4Waves * 1024 : 16];
   extern __shared__ __align__(16) char s_dyn[];    // [tiles][waves][R][16] sums, then x
   float* s_part = reinterpret_cast<float*>(s_dyn);
   const W4Stage st = stage_at(s_dyn + a.tiles * (kW4Waves * R * 64), a.blocks, R);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = threadIdx.x >> 2 & 15, q = threadIdx.x & 3;
+  const int sc16 = R > 1 ? threadIdx.x & 15 : c16;   // the column whose sums the lane takes
   const int n0 = column_tile() * 16 * a.tiles;
   int e = 0;
   int64_t first = 0, rows = a.M;
@@ -442,7 +472,7 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
     };
     auto place = [&](const Piece& p, const u32x4& v) {
       const uint32_t at = lane_x + p.c * (kW4Threads * 16);
-      stage_octet<E>(st, p.m, at >> 4, v, p.m < count && at < (uint32_t)a.blocks * 256);
+      stage_octet<E, R == 1>(st, p.m, at >> 4, v, p.m < count && at < (uint32_t)a.blocks * 256);
     };
     u32x4 xv[XB];
     Piece ask = {0, 0}, put = {0, 0};
@@ -463,7 +493,7 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
     int li = 0, lw = min(s0 * 64, w_last), ls = min((s0 * GP * a.N + n0) * 2 * a.some, s_last);
     auto load = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
       wr = load_codes(src, wo, lw);
-      load_scales<E, GB, Z>(sr, src, c16, ls, a.N * 2, s_last);
+      load_scales<E, GB, Z>(sr, src, sc16, ls, a.N * 2, s_last);
       const bool turn = ++li == steps;
       lw = min(lw + (turn ? w_turn : 64), w_last);
       ls = min(ls + (turn ? s_turn : s_step), s_last);
@@ -483,25 +513,23 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
     }
     for (; put.m < count; next(put)) place(put, fetch(put));
     __syncthreads();
+    static_assert(R == 1 || R == 4, "one row, or four");
     float acc = 0.f;
-    float* mine = s_row + (R > 1 ? wave * R * 64 + (threadIdx.x & 63) : 0);
-    if constexpr (R > 1) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) mine[r * 64] = 0.f;
-    }
     int step = s0, left = steps;   // of the tile in use
-    float* sum = s_part + wave * R * 16 + c16;
+    const int i4 = threadIdx.x >> 2 & 3, k4 = threadIdx.x >> 4 & 3;
+    const int x_row = i4 < count ? i4 : 0, sum_row = k4 < count ? k4 : 0;
+    float* sum = s_part + wave * R * 16 + (R > 1 ? threadIdx.x & 63 : c16);
     auto use = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
-      few_step<E, GB, Z, R>(consts, wr, sr, st, step, count, acc, mine);
+      if constexpr (R == 1)
+        acc += one_row_step<E, GB, Z>(consts, wr, sr, st, step);
+      else
+        acc += four_row_step<E, GB, Z>(consts, wr, sr, st, step, x_row, sum_row,
+                                       s_own + wave * 1024);
       ++step;
       if (--left == 0) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float v = group_sum<4>(R > 1 ? mine[r * 64] : acc);
-          if (q == 0) sum[r * 16] = v;
-          if (R > 1) mine[r * 64] = 0.f;
-          else acc = 0.f;
-        }
+        if constexpr (R == 1) acc = group_sum<4>(acc);
+        if (R > 1 || q == 0) *sum = acc;
+        acc = 0.f;
         sum += kW4Waves * R * 16;
         step = s0;
         left = steps;
@@ -541,13 +569,21 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
 }
 
 // More rows: a wave keeps MT x NT tiles of 16 rows and 16 columns over its part of
-// K, so that each x it reads (from L2) serves 16 NT columns.
+// K, so that each x it reads serves 16 NT columns.  Both operands are loaded in whole
+// lines and take the operands' order through LDS of the wave's own; the next step's
+// loads are in flight meanwhile.
+constexpr int kManyRow = 256 + 16;   // bytes of a row of x in LDS: 16 apart in the banks
+
+constexpr int many_lds(int MT, int NT) {
+  return kManyWaves * (MT * 16 * kManyRow + NT * 1024);
+}
+
 template <typename E, int GB, bool Z, int MT, int NT, W4Mode MODE>
 __global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
-  constexpr int ROWS = 16 * MT, GP = 4 / GB, PF = 2;
-  __shared__ float s_part[kManyWaves][MT][4][64];
-  const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  constexpr int ROWS = 16 * MT, GP = 4 / GB, XL = MT * 4;   // loads of 4 rows
+  extern __shared__ __align__(16) char s_dyn[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, q = lane >> 4;
   const int n0 = column_tile() * 16 * NT;
   int e = 0;
@@ -559,10 +595,13 @@ __global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
     first = x.first;
     rows = x.rows;
   }
+  char* own_x = s_dyn + wave * (MT * 16 * kManyRow + NT * 1024);
+  char* own_w = own_x + MT * 16 * kManyRow;
   const W4Source src = source_of<Z>(a, e, n0, 16 * NT);
-  uint32_t wo[NT];
+  uint32_t wo[NT];   // columns past N read 0
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) wo[nt] = (uint32_t)(nt * 16 + i16) * a.blocks * 64 + q * 16;
+  for (int nt = 0; nt < NT; ++nt)
+    wo[nt] = (uint32_t)(nt * 16 + (lane >> 2)) * a.blocks * 64 + (lane & 3) * 16;
   const int per = (a.blocks + kManyWaves - 1) / kManyWaves;
   const int s0 = min(a.blocks, wave * per), s1 = min(a.blocks, s0 + per);
   const W4Consts<E> consts;
@@ -574,57 +613,70 @@ __global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
     const __amdgpu_buffer_rsrc_t xr =
         resource(static_cast<const char*>(a.x) + from * a.K * 2,
                  (MODE == kGather ? a.M : min((int64_t)ROWS, rows - m0)) * a.K * 2);
-    uint32_t xo[MT];
+    uint32_t xo[XL];   // lane: row lane / 16 of four, 16 bytes lane % 16 of a step's 256
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)   // rows past the last repeat it
-      xo[mt] = (uint32_t)(x_row<MODE>(a, first, min(m0 + mt * 16 + i16, rows - 1)) - from) * a.K * 2 +
-               q * 16;
-    u32x4 w[PF][NT], x[PF][MT][4];
-    W4Scales<E, GB, Z> sc[PF][NT];
-    auto load = [&](int p, int s) {
+    for (int i = 0; i < XL; ++i)   // rows past the last repeat it
+      xo[i] = (uint32_t)(x_row<MODE>(a, first, min(m0 + i * 4 + q, rows - 1)) - from) * a.K * 2 +
+              i16 * 16;
+    u32x4 w[NT], x[XL];
+    W4Scales<E, GB, Z> sc[NT], now[NT];
+    auto load = [&](int s) {
       s = max(min(s, s1 - 1), 0);
+      const int k = s * 128;   // lanes past K: an offset past the resource
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+        x[i] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, k + i16 * 8 < a.K ? xo[i] : kNoX,
+                                                         min(k, max(a.K - 8, 0)) * 2, 0));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        w[p][nt] = load_codes(src, wo[nt], s * 64);
-        load_scales<E, GB, Z>(sc[p][nt], src, i16, (s * GP * a.N + n0 + nt * 16) * 2 * a.some, a.N * 2,
+        w[nt] = load_codes(src, wo[nt], s * 64);
+        load_scales<E, GB, Z>(sc[nt], src, i16, (s * GP * a.N + n0 + nt * 16) * 2 * a.some, a.N * 2,
                               ((a.groups - 1) * a.N + n0 + nt * 16) * 2 * a.some);
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = s * 128 + j * 32;   // past K: an offset past the resource
-          x[p][mt][j] = __builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                         xr, k + q * 8 < a.K ? xo[mt] : kNoX, min(k, max(a.K - 8, 0)) * 2, 0));
-        }
     };
     f32x4 acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto use = [&](int p) {
+    load(s0);
+#pragma clang loop unroll(disable)
+    for (int s = s0; s < s1; ++s) {
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+        *reinterpret_cast<u32x4*>(own_x + (i * 4 + q) * kManyRow + i16 * 16) = x[i];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        loaded(w[p][nt]);
-        sc[p][nt].loaded();
+        const int c = lane >> 2;
+        *reinterpret_cast<u32x4*>(own_w + nt * 1024 +
+                                  (4 * c + (((lane & 3) + (c >> 2)) & 3)) * 16) = w[nt];
+        sc[nt].loaded();
+        now[nt] = sc[nt];
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) loaded(x[p][mt][j]);
+      wave_lds_sync();
       __builtin_amdgcn_sched_barrier(0);
+      load(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      u32x4 v[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        v[nt] = *reinterpret_cast<const u32x4*>(own_w + nt * 1024 +
+                                                (4 * i16 + ((q + (i16 >> 2)) & 3)) * 16);
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
+        u32x4 xv[MT][GB];
         f32x4 xs[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           xs[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int b = 0; b < GB; ++b) xs[mt] = mfma16(E(), x[p][mt][g * GB + b], consts.ones, xs[mt]);
+          for (int b = 0; b < GB; ++b) {
+            xv[mt][b] = *reinterpret_cast<const u32x4*>(own_x + (mt * 16 + i16) * kManyRow +
+                                                        (g * GB + b) * 64 + q * 16);
+            xs[mt] = mfma16(E(), xv[mt][b], consts.ones, xs[mt]);
+          }
         }
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           f32x4 tt[MT];
@@ -632,11 +684,11 @@ __global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
           for (int mt = 0; mt < MT; ++mt) tt[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int b = 0; b < GB; ++b) {
-            const u32x4 c = codes8(consts, w[p][nt][g * GB + b]);
+            const u32x4 c = codes8(consts, v[nt][g * GB + b]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) tt[mt] = mfma16(E(), x[p][mt][g * GB + b], c, tt[mt]);
+            for (int mt = 0; mt < MT; ++mt) tt[mt] = mfma16(E(), xv[mt][b], c, tt[mt]);
           }
-          const float scale = sc[p][nt].scale(g), off = sc[p][nt].offset(g);
+          const float scale = now[nt].scale(g), off = now[nt].offset(g);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -645,42 +697,32 @@ __global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-    };
-#pragma unroll
-    for (int p = 0; p < PF; ++p) {   // on one path and in the loop's order, as in w4_few
-      load(p, s0 + p);
-      __builtin_amdgcn_sched_barrier(0);
+      wave_lds_sync();
     }
-#pragma clang loop unroll(disable)
-    for (int s = s0; s < s1; s += PF) {
-#pragma unroll
-      for (int p = 0; p < PF; ++p) {
-        if (s + p < s1) use(p);
-        __builtin_amdgcn_sched_barrier(0);
-        load(p, s + p + PF);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
+    // the waves' sums, through the same memory
+    static_assert(many_lds(MT, NT) >= kManyWaves * MT * 1024, "room for a tile's sums");
+    float* s_part = reinterpret_cast<float*>(s_dyn);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      __syncthreads();
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s_part[wave][mt][r][lane] = acc[mt][nt][r];
+        for (int r = 0; r < 4; ++r) s_part[((wave * MT + mt) * 4 + r) * 64 + lane] = acc[mt][nt][r];
       __syncthreads();
-      for (int o = t; o < MT * 256; o += kManyThreads) {
+      for (int o = threadIdx.x; o < MT * 256; o += kManyThreads) {
         const int l = o & 63, r = (o >> 6) & 3, mt = o >> 8;
         const int64_t m = m0 + mt * 16 + (l >> 4) * 4 + r;
         const int col = n0 + nt * 16 + (l & 15);
         if (m < rows && col < a.N) {
           float v = 0.f;
 #pragma unroll
-          for (int u = 0; u < kManyWaves; ++u) v += s_part[u][mt][r][l];
+          for (int u = 0; u < kManyWaves; ++u) v += s_part[((u * MT + mt) * 4 + r) * 64 + l];
           store_out<E, MODE>(a, first, m, col, v);
         }
       }
-      __syncthreads();
     }
+    __syncthreads();
   }
 }
 
@@ -763,7 +805,7 @@ __global__ __launch_bounds__(kW4Threads) void w4_scatter_tiny(const W4TinyArgs a
     for (int k = t * 8; k < a.blocks * 128; k += kW4Threads * 8) {
       u32x4 v = {0, 0, 0, 0};
       if (k < a.K) v = *reinterpret_cast<const u32x4*>(xr + k);
-      stage_octet<E>(st, u, k >> 3, v, true);
+      stage_octet<E, true>(st, u, k >> 3, v, true);
     }
   }
   __syncthreads();
@@ -774,7 +816,7 @@ __global__ __launch_bounds__(kW4Threads) void w4_scatter_tiny(const W4TinyArgs a
     W4Stage row = st;
     row.base += cu * st.stride;
     row.sums += cu * (st.sum_stride - st.stride);
-    few_step<E, GB, Z, 1>(consts, wr, sr, row, s0 + ci, 1, acc, nullptr);
+    acc += one_row_step<E, GB, Z>(consts, wr, sr, row, s0 + ci);
     if (++ci == steps) {
       const float v = group_sum<4>(acc);
       if (q == 0) s_part[wave][cu][c16] = v;
@@ -852,12 +894,13 @@ __global__ __launch_bounds__(256) void w4_pack(int64_t n_matrices, int64_t K, in
 constexpr int64_t kFewLds = 128 << 10;   // most LDS that x may take
 
 // Column tiles of a block: one until there are blocks enough to fill the chip a
-// few times over, then up to 8, which spread a block's fixed costs.
+// few times over, then up to 8, which spread a block's fixed costs (4096 x 2816,
+// 61 tokens over 64 experts: 1 tile 160 us, 2 119, 4 110, 8 108; 8 experts: 1 tile
+// 22.7 us, 2 21.5, 4 23).
+constexpr int64_t kFewBlocks = 1024;
 int few_tiles(int64_t blocks) {
-  static const char* env = getenv("FM_T");
-  const int64_t target = env ? atoi(env) : 1024;
   int t = 1;
-  while (t < 8 && blocks / (2 * t) >= target) t *= 2;
+  while (t < 8 && blocks / (2 * t) >= kFewBlocks) t *= 2;
   return t;
 }
 
@@ -875,7 +918,8 @@ void launch_rows(W4Args a, int64_t most, dim3 grid, hipStream_t stream) {
   do {                                                                                       \
     if (MODE <= kDense32) grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, 16 * MT), 65535);   \
     grid.x = (unsigned)cdiv(a.N, 16 * NT);                                                   \
-    hipLaunchKernelGGL((w4_many<E, GB, Z, MT, NT, MODE>), grid, dim3(kManyThreads), 0, stream, a); \
+    hipLaunchKernelGGL((w4_many<E, GB, Z, MT, NT, MODE>), grid, dim3(kManyThreads),          \
+                       many_lds(MT, NT), stream, a);                                         \
   } while (0)
   if constexpr (MODE == kGather) {
     if (a.n_pairs > 0) {
@@ -890,7 +934,7 @@ void launch_rows(W4Args a, int64_t most, dim3 grid, hipStream_t stream) {
   else if (most <= 8 && stage_bytes(a.blocks, 4) <= kFewLds) FM_FEW(4, false);
   else if (most <= 16) FM_MANY(1, 2);
   else if (most <= 32) FM_MANY(2, 2);
-  else FM_MANY(3, 2);
+  else FM_MANY(3, 3);
 #undef FM_FEW
 #undef FM_MANY
 }

@@ -73,6 +73,13 @@ __device__ __forceinline__ float group_max(float x) {
   }
 }
 
+// LDS traffic between the lanes of one wave: the wave's LDS operations complete
+// in order, so only the compiler has to keep them so.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Element types of a row: F32 beside the 16-bit formats.
 struct F32 {
   static constexpr fm_dtype_t id = FM_F32;
