@@ -18,6 +18,7 @@ constexpr int kGateWaves = kGateThreads / 64;
 constexpr int kGateMaxExperts = 1024;
 constexpr int kGateMaxTopk = 16;
 constexpr int kGateMaxBlocks = 512;     // blocks whose partial sums are joined
+constexpr int kGateBatch = 36;          // loads in flight of the join: 512 blocks of 64 experts at once
 constexpr int kGateFinishThreads = 1024;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -328,11 +329,18 @@ __global__ __launch_bounds__(kGateFinishThreads) void gate_join(const GateArgs a
   for (int i = t; i < S * C; i += kGateFinishThreads) {
     GatePart sum = {0.f, 0};
     const GatePart* from = a.part + i % C;
-#pragma unroll 16
-    for (int b = i / C; b < blocks; b += S) {
-      const GatePart p = from[(int64_t)b * C];
-      sum.sum += p.sum;
-      sum.count += p.count;
+    // kGateBatch loads in flight; past the last block that one again, not added
+    for (int b0 = i / C; b0 < blocks; b0 += kGateBatch * S) {
+      GatePart p[kGateBatch];
+#pragma unroll
+      for (int u = 0; u < kGateBatch; ++u)
+        p[u] = from[(int64_t)min(b0 + u * S, blocks - 1) * C];
+#pragma unroll
+      for (int u = 0; u < kGateBatch; ++u) {
+        const bool in = b0 + u * S < blocks;
+        sum.sum += in ? p[u].sum : 0.f;
+        sum.count += in ? p[u].count : 0;
+      }
     }
     s_part[i] = sum;
   }
@@ -406,18 +414,33 @@ __global__ __launch_bounds__(kGateThreads) void gate_bwd(const GateBwdArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) x[v] = kNegInf;
     }
-    // the slots' inputs
+    // The slots' inputs: ids and gradients come with the row, the chosen logits
+    // from the row's copy in LDS (from memory they would be a second wait).
     if (a.d_weights) {
       for (int i = lane; i < G * topk; i += 64) {
         const int q = wave * G + i / topk, k = i % topk;
         const int64_t at = base + q;
-        const bool in = at < a.T && (!a.mask || a.mask[at] != 0);
-        int id = in ? a.ids[at * topk + k] : -1;
+        int id = -1;
+        float d = 0.f;
+        if (at < a.T) {
+          id = a.ids[at * topk + k];
+          d = a.d_weights[at * topk + k] * a.scale;
+          if (a.mask && a.mask[at] == 0) id = -1;
+        }
         if ((unsigned)id >= (unsigned)n) id = -1;
         s_id[q][k] = id;
-        s_x[q][k] = id >= 0 ? (float)logits[at * n + id] : kNegInf;
-        s_d[q][k] = id >= 0 ? a.d_weights[at * topk + k] * a.scale : 0.f;
+        s_d[q][k] = id >= 0 ? d : 0.f;
       }
+#pragma unroll
+      for (int c = 0; c < V / 4; ++c)
+        *reinterpret_cast<f32x4*>(&s_du[r][(c * LPR + sub) * 4]) =
+            f32x4{x[c * 4], x[c * 4 + 1], x[c * 4 + 2], x[c * 4 + 3]};
+      wave_lds_sync();
+      for (int i = lane; i < G * topk; i += 64) {
+        const int q = wave * G + i / topk, k = i % topk, id = s_id[q][k];
+        s_x[q][k] = id >= 0 ? s_du[q][id] : kNegInf;
+      }
+      wave_lds_sync();
     }
     float m = x[0];
 #pragma unroll
