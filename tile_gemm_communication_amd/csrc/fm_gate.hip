@@ -13,12 +13,14 @@
 namespace fm {
 namespace {
 
-constexpr int kGateThreads = 256;
+constexpr int kGateThreads = 512;       // forward: few blocks, whose partial sums one block joins
 constexpr int kGateWaves = kGateThreads / 64;
+constexpr int kGateBwdThreads = 256;
+constexpr int kGateBwdWaves = kGateBwdThreads / 64;
 constexpr int kGateMaxExperts = 1024;
 constexpr int kGateMaxTopk = 16;
-constexpr int kGateMaxBlocks = 512;     // blocks whose partial sums are joined
-constexpr int kGateBatch = 36;          // loads in flight of the join: 512 blocks of 64 experts at once
+constexpr int kGateMaxBlocks = 256;     // blocks whose partial sums are joined
+constexpr int kGateBatch = 18;          // loads in flight of the join: 256 blocks of 64 experts at once
 constexpr int kGateFinishThreads = 1024;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -59,6 +61,25 @@ __device__ __forceinline__ void share_nums(const float (&x)[V], bool sigmoid, fl
       }
     }
   }
+}
+
+// Sum over the groups of LPR lanes of a wave, lane by lane, right in group 0.
+template <int LPR>
+__device__ __forceinline__ float sum_over_groups(float x) {
+  auto rotated = [](float v, auto ctrl) {
+    return __builtin_bit_cast(float, dpp<decltype(ctrl)::value>(__builtin_bit_cast(int, v)));
+  };
+  if constexpr (LPR <= 8) x += rotated(x, std::integral_constant<int, 0x128>());   // row_ror:8
+  if constexpr (LPR <= 4) x += rotated(x, std::integral_constant<int, 0x124>());   // row_ror:4
+  if constexpr (LPR <= 16) {
+    const LanePair<float> p = lane_pair<16>(x);
+    x = p.a + p.b;
+  }
+  if constexpr (LPR <= 32) {
+    const LanePair<float> p = lane_pair<32>(x);
+    x = p.a + p.b;
+  }
+  return x;
 }
 
 // The expert of slot v of a lane: V / 4 chunks of 4, chunk c at (c * LPR + sub) * 4.
@@ -143,7 +164,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
   __shared__ int s_id[RP][kGateMaxTopk];
   __shared__ float s_m[RP], s_inv[RP];
   __shared__ int s_cnt[LPR * V + 1];
-  __shared__ float s_sum[RP * LPR * V];
+  __shared__ __align__(16) float s_sum[kGateWaves][LPR * V];
   __shared__ double s_loss[kGateWaves];
   typedef typename std::conditional<BIAS, double, float>::type Key;
 
@@ -300,11 +321,18 @@ __global__ __launch_bounds__(kGateThreads) void gate_fwd(const GateArgs a) {
   tokens = group_sum<64>(tokens);
   if (lane == 0) atomicAdd(&s_cnt[n], tokens);
 #pragma unroll
-  for (int v = 0; v < V; ++v) s_sum[r * LPR * V + slot_expert<LPR>(v, sub)] = acc[v];
+  for (int v = 0; v < V; ++v) acc[v] = sum_over_groups<LPR>(acc[v]);
+  if (grp == 0) {
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c)
+      *reinterpret_cast<f32x4*>(&s_sum[wave][(c * LPR + sub) * 4]) =
+          f32x4{acc[c * 4], acc[c * 4 + 1], acc[c * 4 + 2], acc[c * 4 + 3]};
+  }
   __syncthreads();
   auto block_sum = [&](int e) {
     float s = 0.f;
-    for (int q = 0; q < RP; ++q) s += s_sum[q * LPR * V + e];
+#pragma unroll
+    for (int w = 0; w < kGateWaves; ++w) s += s_sum[w][e];
     return s;
   };
   if (gridDim.x == 1) {
@@ -379,10 +407,10 @@ struct GateBwdArgs {
 //          w_k d_k, less p * sum w d for a softmax score
 //   dx = du (softmax) or du * sigmoid(-x).
 template <typename E, int LPR, int V, bool SIGMOID>
-__global__ __launch_bounds__(kGateThreads) void gate_bwd(const GateBwdArgs a) {
+__global__ __launch_bounds__(kGateBwdThreads) void gate_bwd(const GateBwdArgs a) {
   typedef typename Elem<E>::type L;
   constexpr int G = 64 / LPR;
-  constexpr int RP = G * kGateWaves;
+  constexpr int RP = G * kGateBwdWaves;
   __shared__ float s_x[RP][kGateMaxTopk], s_d[RP][kGateMaxTopk], s_c[RP][kGateMaxTopk];
   __shared__ int s_id[RP][kGateMaxTopk];
   __shared__ float s_m[RP], s_inv[RP];
@@ -701,14 +729,14 @@ extern "C" fm_status_t fm_moe_gate_bwd(fm_dtype_t dt, int64_t T, int32_t n_exper
   a.topk = topk;
   a.renorm = renormalize;
   a.scale = scale;
-  const int blocks = (int)std::min<int64_t>(cdiv(T, kGateThreads / gate_lanes(n_experts)), 2048);
+  const int blocks = (int)std::min<int64_t>(cdiv(T, kGateBwdThreads / gate_lanes(n_experts)), 2048);
 #define FM_GATE_CALL(LPR, V)                                                                  \
   do {                                                                                        \
     if (score == FM_GATE_SIGMOID)                                                             \
-      hipLaunchKernelGGL((gate_bwd<FM_E, LPR, V, true>), dim3(blocks), dim3(kGateThreads), 0, \
+      hipLaunchKernelGGL((gate_bwd<FM_E, LPR, V, true>), dim3(blocks), dim3(kGateBwdThreads), 0, \
                          stream, a);                                                          \
     else                                                                                      \
-      hipLaunchKernelGGL((gate_bwd<FM_E, LPR, V, false>), dim3(blocks), dim3(kGateThreads), 0, \
+      hipLaunchKernelGGL((gate_bwd<FM_E, LPR, V, false>), dim3(blocks), dim3(kGateBwdThreads), 0, \
                          stream, a);                                                          \
   } while (0)
   if (dt == FM_F16) {
