@@ -247,14 +247,45 @@ def test_pack_refusals_and_sizes():
     assert fm.fm_norm_residual_workspace_bytes(16, 64, 4) > 0
 
 
+def _native():
+    pytest.importorskip("torch")
+    fm.lib()
+    from tile_gemm_communication_amd import _fluxmi
+    return _fluxmi
+
+
 def test_binding_refuses_tensors_it_cannot_pass():
-    torch = pytest.importorskip("torch")
-    if torch.cuda.is_available():
-        pytest.skip("host tensors are refused by their device there as well")
-    x = torch.zeros(4, 8)
-    with pytest.raises((ValueError, RuntimeError, AssertionError)):
-        fm.fm_moe_gate(x, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))
+    """The checks stand before any call of the library, so host tensors do."""
+    import torch
+    m = _native()
+    x, i = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+
+    def refused(error, text, f, *args):
+        with pytest.raises(error, match=text):
+            f(0, 0, *args)
+
+    refused(ValueError, "logits must live on the current GPU", m.moe_gate, x, i, torch.zeros(4, 2), 0,
+            0, 1.0, None, None, None, None, None, None)
+    refused(TypeError, "unsupported dtype", m.moe_gate, x.double(), i, x, 0, 0, 1.0, None, None, None,
+            None, None, None)
+    refused(TypeError, "logits must be a tensor", m.moe_gate, 3, i, x, 0, 0, 1.0, None, None, None,
+            None, None, None)
+    refused(ValueError, "topk_ids must be a matrix", m.moe_gate_bwd, x, None, x, 0, 0, 1.0, None, None,
+            None, None)
+    refused(ValueError, "must live", m.norm_residual, x, None, None, x, None, None, None, 1.0, 1e-6,
+            None, None)
+    refused(ValueError, "block or resid must be a matrix", m.norm_residual, None, None, None, None,
+            None, None, None, 1.0, 1e-6, None, None)
+    refused(ValueError, "group must be", m.gemm_w4, x, x, x, x, 48, None)
+    refused(ValueError, "packed must have three dimensions", m.moe_gather_gemm_w4, x, i, x, x, x, i, i,
+            0, 32, None, None, 0)
+    refused(ValueError, "too short", m.moe_gather_gemm_w4, x, i, torch.zeros(2, 8, 64), x, x, i[:, 0],
+            i, 0, 32, None, None, 0)
+    with pytest.raises(TypeError, match="wrong number"):
+        m.gemm_w4(0, 0)
     with pytest.raises(ValueError):
         fm.fm_norm_residual(None, None, resid=x)
     with pytest.raises(ValueError):
-        fm.fm_gemm_w4(x, x, x, torch.zeros(3, 8), 48)
+        fm.fm_norm_residual_bwd(x, None)
+    with pytest.raises(ValueError):
+        fm.fm_w4_pack(x, x)

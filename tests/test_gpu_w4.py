@@ -298,3 +298,21 @@ def test_w4_agrees_with_the_16_bit_layer():
         outs.append((h, out))
     d = (outs[0][1] - outs[1][1]).double()
     assert d.norm() <= 4e-6 * outs[0][1].double().norm()
+
+
+def test_tensors_the_kernels_cannot_take_are_refused():
+    import torch
+    x = torch.zeros(2, 256, device="cuda:0", dtype=torch.bfloat16)
+    p = torch.zeros(16, 128, device="cuda:0", dtype=torch.uint8)
+    s, c = torch.zeros(8, 16, device="cuda:0", dtype=torch.bfloat16), torch.zeros(2, 16, device="cuda:0")
+    good = dict(A=x, packed=p, scales=s, C=c, group=32)
+    fm.fm_gemm_w4(**good)
+    for name, bad in (("A", x.float()), ("A", x[:, ::2]), ("packed", p[:, :64]), ("packed", p.int()),
+                      ("scales", s[:4]), ("scales", s.half()), ("scales", s.cpu()), ("C", c.double()),
+                      ("C", torch.zeros(3, 16, device="cuda:0")), ("group", 64), ("group", 16)):
+        with pytest.raises((ValueError, TypeError)):
+            fm.fm_gemm_w4(**{**good, name: bad})
+    with pytest.raises(fm.FluxMIError):      # 16-bit output of another type: refused by the library
+        fm.fm_gemm_w4(x, p, s, c.half(), 32)
+    with pytest.raises(fm.FluxMIError):      # a row that starts between 16-byte boundaries
+        fm.fm_gemm_w4(x.view(-1)[4:260].view(1, 256), p, s, c[:1], 32)

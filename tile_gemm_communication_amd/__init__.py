@@ -491,18 +491,23 @@ def fm_probe_mfma(dtype, mfma16: bool, waves_per_simd: int, iters: int, zero: bo
 # -- around the block: router, norms, 4-bit weights --------------------------------
 #
 # A decode step makes these calls one token at a time, so what the binding costs
-# counts: each tensor is looked at once, and torch's own names are kept in _RT.
+# counts: _fluxmi (csrc/fm_python.cpp) looks at the tensors and calls the library.
+# It raises ValueError or TypeError for tensors of another type, shape, layout or
+# device than the current one, before the library is called.
 
 class _Runtime:
     def __init__(self):
         torch = _torch()
-        self.f16, self.bf16, self.f32 = torch.float16, torch.bfloat16, torch.float32
-        self.i32, self.u8 = torch.int32, torch.uint8
-        self.code = {torch.float16: FM_F16, torch.bfloat16: FM_BF16, torch.float32: FM_F32}
         torch.cuda.current_device()   # initialises the device, or says why not
         self.device = torch._C._cuda_getDevice
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
-        self.lib = lib()
+        self.stream = torch._C._cuda_getCurrentRawStream
+        lib()
+        try:
+            from . import _fluxmi
+        except ImportError as e:
+            raise ImportError(f"{_HERE}/_fluxmi.so cannot be loaded ({e}); build it with "
+                              "`python tile_gemm_communication_amd/build.py`") from e
+        self.native = _fluxmi
 
 
 _RT = None
@@ -513,38 +518,6 @@ def _rt() -> _Runtime:
     if _RT is None:
         _RT = _Runtime()
     return _RT
-
-
-def _arg(fn: str, name: str, t, dtype, shape, device: int):
-    """The address of a tensor that has this type and shape, is contiguous and
-    lies on `device`; None for None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{fn}: {name} must be {dtype} {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{fn}: {name} must live on the current GPU")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be contiguous")
-    return t.data_ptr()
-
-
-def _ws_arg(fn: str, ws, device: int):
-    if ws is None:
-        return None, 0
-    return _arg(fn, "ws", ws, ws.dtype, ws.shape, device), ws.nbytes
-
-
-def _code(rt, dtype) -> int:
-    c = rt.code.get(dtype)
-    if c is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return c
-
-
-def _on(rt, device: int, stream):
-    return rt.raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def _scratch(fn: str, n: int, device):
@@ -570,22 +543,13 @@ def fm_moe_gate(logits, topk_ids, topk_weights, score: int = FM_GATE_SOFTMAX,
                 counts=None, prob_sums=None, loss=None, ws=None, stream=None) -> None:
     """topk_ids, topk_weights [T, topk] from logits [T, E]; with counts [E + 1],
     prob_sums [E] and loss [1] (all or none) the expert counts and balance loss."""
-    fn, rt = "fm_moe_gate", _rt()
+    rt = _rt()
     d = rt.device()
-    T, E = logits.shape
-    topk = topk_ids.shape[1]
-    wp, wn = _ws_arg(fn, ws, d)
-    st = rt.lib.fm_moe_gate(
-        _code(rt, logits.dtype), T, E, topk, score, 1 if renormalize else 0, scale,
-        _arg(fn, "logits", logits, logits.dtype, (T, E), d), _arg(fn, "bias", bias, rt.f32, (E,), d),
-        _arg(fn, "token_mask", token_mask, rt.u8, (T,), d),
-        _arg(fn, "topk_ids", topk_ids, rt.i32, (T, topk), d),
-        _arg(fn, "topk_weights", topk_weights, rt.f32, (T, topk), d),
-        _arg(fn, "counts", counts, rt.i32, (E + 1,), d),
-        _arg(fn, "prob_sums", prob_sums, rt.f32, (E,), d), _arg(fn, "loss", loss, rt.f32, (1,), d),
-        wp, wn, _on(rt, d, stream))
+    st = rt.native.moe_gate(d, rt.stream(d) if stream is None else stream.cuda_stream, logits,
+                            topk_ids, topk_weights, score, 1 if renormalize else 0, scale, bias,
+                            token_mask, counts, prob_sums, loss, ws)
     if st:
-        raise FluxMIError(fn, st)
+        raise FluxMIError("fm_moe_gate", st)
 
 
 def fm_moe_gate_bwd(logits, topk_ids, d_logits, score: int = FM_GATE_SOFTMAX,
@@ -593,38 +557,13 @@ def fm_moe_gate_bwd(logits, topk_ids, d_logits, score: int = FM_GATE_SOFTMAX,
                     d_weights=None, counts=None, d_loss=None, stream=None) -> None:
     """d_logits [T, E] from d_weights [T, topk] (gradient of topk_weights) and
     d_loss [1] (gradient of the loss, with fm_moe_gate's counts)."""
-    fn, rt = "fm_moe_gate_bwd", _rt()
+    rt = _rt()
     d = rt.device()
-    T, E = logits.shape
-    topk = topk_ids.shape[1]
-    st = rt.lib.fm_moe_gate_bwd(
-        _code(rt, logits.dtype), T, E, topk, score, 1 if renormalize else 0, scale,
-        _arg(fn, "logits", logits, logits.dtype, (T, E), d),
-        _arg(fn, "token_mask", token_mask, rt.u8, (T,), d),
-        _arg(fn, "topk_ids", topk_ids, rt.i32, (T, topk), d),
-        _arg(fn, "d_weights", d_weights, rt.f32, (T, topk), d),
-        _arg(fn, "counts", counts, rt.i32, (E + 1,), d),
-        _arg(fn, "d_loss", d_loss, rt.f32, (1,), d),
-        _arg(fn, "d_logits", d_logits, logits.dtype, (T, E), d), _on(rt, d, stream))
+    st = rt.native.moe_gate_bwd(d, rt.stream(d) if stream is None else stream.cuda_stream,
+                                logits, topk_ids, d_logits, score, 1 if renormalize else 0, scale,
+                                token_mask, d_weights, counts, d_loss)
     if st:
-        raise FluxMIError(fn, st)
-
-
-def _first_dtype(*tensors):
-    for t in tensors:
-        if t is not None:
-            return t.dtype
-    return None
-
-
-def _norm_dtypes(rt, small, streams, blocks):
-    """(dt, stream_dt, block_dt) from the 16-bit operands, the residual stream's
-    tensors and the block's; where there is no 16-bit operand, from the others."""
-    sd, bd = _first_dtype(*streams), _first_dtype(*blocks)
-    dt = _first_dtype(*small)
-    if dt is None:
-        dt = next((x for x in (sd, bd) if x is not None and x is not rt.f32), rt.bf16)
-    return dt, dt if sd is None else sd, dt if bd is None else bd
+        raise FluxMIError("fm_moe_gate_bwd", st)
 
 
 def fm_norm_residual(out, y, block=None, resid=None, w_post=None, w_pre=None, gate=None,
@@ -632,25 +571,15 @@ def fm_norm_residual(out, y, block=None, resid=None, w_post=None, w_pre=None, ga
                      stream=None) -> None:
     """out = resid + scale * gate * (norm(block) * w_post), y = norm(out) * w_pre;
     out or y may be None (not wanted), as may every operand (see fluxmi.h)."""
-    fn = "fm_norm_residual"
-    like = resid if block is None else block
-    if like is None or (out is None and y is None):
+    if (block is None and resid is None) or (out is None and y is None):
         raise ValueError("fm_norm_residual: block or resid, and out or y, are needed")
     rt = _rt()
-    d, f32 = rt.device(), rt.f32
-    dt, sd, bd = _norm_dtypes(rt, (y, w_pre, w_post, gate), (resid, out), (block,))
-    shape = like.shape
-    M, N = shape
-    G = 0 if gate is None else gate.shape[0]
-    st = rt.lib.fm_norm_residual(
-        _code(rt, dt), _code(rt, sd), _code(rt, bd), M, N, _arg(fn, "block", block, bd, shape, d),
-        _arg(fn, "resid", resid, sd, shape, d), _arg(fn, "w_post", w_post, dt, (N,), d),
-        _arg(fn, "w_pre", w_pre, dt, (N,), d), _arg(fn, "gate", gate, dt, (G, N), d), G, scale, eps,
-        _arg(fn, "out", out, sd, shape, d), _arg(fn, "y", y, dt, shape, d),
-        _arg(fn, "rstd_post", rstd_post, f32, (M,), d), _arg(fn, "rstd_pre", rstd_pre, f32, (M,), d),
-        _on(rt, d, stream))
+    d = rt.device()
+    st = rt.native.norm_residual(d, rt.stream(d) if stream is None else stream.cuda_stream,
+                                 out, y, block, resid, w_post, w_pre, gate, scale, eps, rstd_post,
+                                 rstd_pre)
     if st:
-        raise FluxMIError(fn, st)
+        raise FluxMIError("fm_norm_residual", st)
 
 
 def fm_norm_residual_workspace_bytes(M: int, N: int, n_gates: int = 0) -> int:
@@ -670,29 +599,15 @@ def fm_norm_residual_bwd(d_resid, d_block, out=None, block=None, d_y=None, d_out
                          stream=None) -> None:
     """Gradients of fm_norm_residual; each of d_resid, d_block, d_w_post,
     d_w_pre and d_gate may be None (not wanted)."""
-    fn = "fm_norm_residual_bwd"
-    like = d_out if d_y is None else d_y
-    if like is None:
+    if d_y is None and d_out is None:
         raise ValueError("fm_norm_residual_bwd: d_y or d_out is needed")
     rt = _rt()
-    d, f32 = rt.device(), rt.f32
-    dt, sd, bd = _norm_dtypes(rt, (d_y, w_pre, w_post, gate), (d_out, out, d_resid),
-                              (block, d_block))
-    shape = like.shape
-    M, N = shape
-    G = 0 if gate is None else gate.shape[0]
-    wp, wn = _ws_arg(fn, ws, d)
-    st = rt.lib.fm_norm_residual_bwd(
-        _code(rt, dt), _code(rt, sd), _code(rt, bd), M, N, _arg(fn, "d_y", d_y, dt, shape, d),
-        _arg(fn, "d_out", d_out, sd, shape, d), _arg(fn, "out", out, sd, shape, d),
-        _arg(fn, "block", block, bd, shape, d), _arg(fn, "w_post", w_post, dt, (N,), d),
-        _arg(fn, "w_pre", w_pre, dt, (N,), d), _arg(fn, "gate", gate, dt, (G, N), d), G, scale,
-        _arg(fn, "rstd_post", rstd_post, f32, (M,), d), _arg(fn, "rstd_pre", rstd_pre, f32, (M,), d),
-        _arg(fn, "d_resid", d_resid, sd, shape, d), _arg(fn, "d_block", d_block, bd, shape, d),
-        _arg(fn, "d_w_post", d_w_post, f32, (N,), d), _arg(fn, "d_w_pre", d_w_pre, f32, (N,), d),
-        _arg(fn, "d_gate", d_gate, f32, (G, N), d), wp, wn, _on(rt, d, stream))
+    d = rt.device()
+    st = rt.native.norm_residual_bwd(d, rt.stream(d) if stream is None else stream.cuda_stream,
+                                     d_resid, d_block, out, block, d_y, d_out, w_post, w_pre, gate,
+                                     scale, rstd_post, rstd_pre, d_w_post, d_w_pre, d_gate, ws)
     if st:
-        raise FluxMIError(fn, st)
+        raise FluxMIError("fm_norm_residual_bwd", st)
 
 
 def fm_w4_row_bytes(K: int) -> int:
@@ -702,41 +617,28 @@ def fm_w4_row_bytes(K: int) -> int:
 
 def fm_w4_pack(codes, packed, stream=None) -> None:
     """Codes uint8 [..., K, N] (0..15) into packed uint8 [..., N, fm_w4_row_bytes(K)]."""
-    fn, rt = "fm_w4_pack", _rt()
-    d = rt.device()
+    torch = _torch()
     lead, (K, N) = tuple(codes.shape[:-2]), codes.shape[-2:]
     n = 1
     for x in lead:
         n *= x
-    st = rt.lib.fm_w4_pack(n, K, N, _arg(fn, "codes", codes, rt.u8, codes.shape, d),
-                           _arg(fn, "packed", packed, rt.u8, lead + (N, -(-K // 128) * 64), d),
-                           _on(rt, d, stream))
-    if st:
-        raise FluxMIError(fn, st)
-
-
-def _w4_groups(fn: str, K: int, group: int) -> int:
-    if group not in (32, 64, 128):
-        raise ValueError(f"{fn}: group must be 32, 64 or 128")
-    return -(-K // group)
+    if (codes.dtype != torch.uint8 or packed.dtype != torch.uint8
+            or tuple(packed.shape) != lead + (N, fm_w4_row_bytes(K))):
+        raise ValueError("fm_w4_pack: shape or dtype mismatch")
+    if codes.device != packed.device or codes.device.index != torch.cuda.current_device():
+        raise ValueError("fm_w4_pack: tensors must live on the current GPU")
+    _check("fm_w4_pack", lib().fm_w4_pack(n, K, N, _ptr(codes), _ptr(packed), _stream(stream)))
 
 
 def fm_gemm_w4(A, packed, scales, C, group: int, zeros=None, stream=None) -> None:
     """C = A @ W, W [K, N] held as 4-bit codes with scales [ceil(K / group), N]
     (and zeros of that shape, 8 without them)."""
-    fn = "fm_gemm_w4"
-    M, K = A.shape
-    N = C.shape[1]
-    shape = (_w4_groups(fn, K, group), N)
     rt = _rt()
-    d, dt = rt.device(), A.dtype
-    st = rt.lib.fm_gemm_w4(
-        _code(rt, dt), _code(rt, C.dtype), M, N, K, group, _arg(fn, "A", A, dt, (M, K), d),
-        _arg(fn, "packed", packed, rt.u8, (N, -(-K // 128) * 64), d),
-        _arg(fn, "scales", scales, dt, shape, d), _arg(fn, "zeros", zeros, rt.u8, shape, d),
-        _arg(fn, "C", C, C.dtype, (M, N), d), _on(rt, d, stream))
+    d = rt.device()
+    st = rt.native.gemm_w4(d, rt.stream(d) if stream is None else stream.cuda_stream, A, packed,
+                           scales, C, group, zeros)
     if st:
-        raise FluxMIError(fn, st)
+        raise FluxMIError("fm_gemm_w4", st)
 
 
 def fm_moe_gather_gemm_w4(X, topk_ids, packed, scales, H, sorted_pairs, expert_offsets,
@@ -744,27 +646,13 @@ def fm_moe_gather_gemm_w4(X, topk_ids, packed, scales, H, sorted_pairs, expert_o
                           stream=None) -> None:
     """Route, then H[rows of expert e] = act(X[gathered tokens] @ W1[e]), W1
     [n_local, hidden, ffn] in 4 bits."""
-    fn = "fm_moe_gather_gemm_w4"
-    T, hidden = X.shape
-    topk, nl = topk_ids.shape[1], packed.shape[0]
-    rows, ffn = H.shape
-    pairs = sorted_pairs.shape
-    if rows < T * topk or len(pairs) != 1 or pairs[0] < T * topk:
-        raise ValueError(f"{fn}: H or sorted_pairs is too short")
-    shape = (nl, _w4_groups(fn, hidden, group), ffn)
     rt = _rt()
-    d, dt = rt.device(), X.dtype
-    wp, wn = _ws_arg(fn, ws, d)
-    st = rt.lib.fm_moe_gather_gemm_w4(
-        _code(rt, dt), T, hidden, ffn, topk, expert_begin, nl, group,
-        _arg(fn, "X", X, dt, (T, hidden), d), _arg(fn, "topk_ids", topk_ids, rt.i32, (T, topk), d),
-        _arg(fn, "packed", packed, rt.u8, (nl, ffn, -(-hidden // 128) * 64), d),
-        _arg(fn, "scales", scales, dt, shape, d), _arg(fn, "zeros", zeros, rt.u8, shape, d),
-        _arg(fn, "H", H, dt, (rows, ffn), d), _arg(fn, "sorted_pairs", sorted_pairs, rt.i32, pairs, d),
-        _arg(fn, "expert_offsets", expert_offsets, rt.i32, (nl + 1,), d), act, wp, wn,
-        _on(rt, d, stream))
+    d = rt.device()
+    st = rt.native.moe_gather_gemm_w4(d, rt.stream(d) if stream is None else stream.cuda_stream,
+                                       X, topk_ids, packed, scales, H, sorted_pairs,
+                                       expert_offsets, expert_begin, group, ws, zeros, act)
     if st:
-        raise FluxMIError(fn, st)
+        raise FluxMIError("fm_moe_gather_gemm_w4", st)
 
 
 def fm_moe_w4_workspace_bytes(T: int, topk: int, hidden: int) -> int:
@@ -783,27 +671,10 @@ def fm_moe_gemm_scatter_w4(H, packed, scales, topk_ids, sorted_pairs, expert_off
                            add=None, stream=None) -> None:
     """out[t] = add[t] + sum_k w[t,k] * (H[row(t,k)] @ W2[e(t,k)]) over local
     pairs, W2 [n_local, ffn, hidden] in 4 bits."""
-    fn = "fm_moe_gemm_scatter_w4"
-    T, topk = topk_weights.shape
-    rows, ffn = H.shape
-    hidden, nl = out.shape[1], packed.shape[0]
-    pairs = sorted_pairs.shape
-    if rows < T * topk or len(pairs) != 1 or pairs[0] < T * topk:
-        raise ValueError(f"{fn}: H or sorted_pairs is too short")
-    shape = (nl, _w4_groups(fn, ffn, group), hidden)
     rt = _rt()
-    d, dt, i32, f32 = rt.device(), H.dtype, rt.i32, rt.f32
-    wp, wn = _ws_arg(fn, ws, d)
-    st = rt.lib.fm_moe_gemm_scatter_w4(
-        _code(rt, dt), T, hidden, ffn, topk, expert_begin, nl, group,
-        _arg(fn, "H", H, dt, (rows, ffn), d),
-        _arg(fn, "packed", packed, rt.u8, (nl, hidden, -(-ffn // 128) * 64), d),
-        _arg(fn, "scales", scales, dt, shape, d), _arg(fn, "zeros", zeros, rt.u8, shape, d),
-        _arg(fn, "topk_ids", topk_ids, i32, (T, topk), d),
-        _arg(fn, "sorted_pairs", sorted_pairs, i32, pairs, d),
-        _arg(fn, "expert_offsets", expert_offsets, i32, (nl + 1,), d),
-        _arg(fn, "topk_weights", topk_weights, f32, (T, topk), d),
-        _arg(fn, "add", add, f32, (T, hidden), d), _arg(fn, "out", out, f32, (T, hidden), d), wp, wn,
-        _on(rt, d, stream))
+    d = rt.device()
+    st = rt.native.moe_gemm_scatter_w4(d, rt.stream(d) if stream is None else stream.cuda_stream,
+                                        H, packed, scales, topk_ids, sorted_pairs, expert_offsets,
+                                        topk_weights, out, expert_begin, group, ws, zeros, add)
     if st:
-        raise FluxMIError(fn, st)
+        raise FluxMIError("fm_moe_gemm_scatter_w4", st)

@@ -1,7 +1,8 @@
-"""Build libfluxmi.so (HIP, gfx950 only) in-tree.
+"""Build libfluxmi.so (HIP, gfx950 only) and the binding's module in-tree.
 
 Every source under csrc/ is compiled by hipcc for gfx950 and linked into one
-shared library next to this file, which the Python binding loads.  Packed
+shared library next to this file, which the Python binding loads; _fluxmi.so
+(host code against torch's headers) checks tensors for it.  Packed
 fp32 VALU ops are disabled for every device compile.  The compiler's
 per-kernel register and scratch figures are kept in
 _build/kernel_resources.json, which the CPU tests check.
@@ -22,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfluxmi.so")
+MODULE = os.path.join(HERE, "_fluxmi.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -64,12 +66,45 @@ def _compile(src: str):
     return obj, _resources(r.stderr)
 
 
+def _compile_module() -> str:
+    """The host object of fm_python.cpp (torch and Python headers)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    obj = os.path.join(BUILD_DIR, "fm_python.o")
+    flags = [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM", "-O2", "-std=c++17", "-fPIC", "-w"]
+    dirs = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths(),
+            os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include")]
+    cmd = ["g++", *flags, *[x for d in dirs for x in ("-I", d)], "-c",
+           os.path.join(CSRC, "fm_python.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for fm_python.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_module(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MODULE + ".tmp"
+    cmd = ["g++", "-shared", "-fPIC", obj, "-o", tmp, "-L", HERE, "-l:libfluxmi.so",
+           "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MODULE)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
-    jobs = min(len(srcs), int(os.environ.get("MAX_JOBS", "8")))
+    jobs = min(len(srcs) + 1, int(os.environ.get("MAX_JOBS", "8")))
     with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
+        module = ex.submit(_compile_module)
         done = list(ex.map(_compile, srcs))
+        module = module.result()
     objs = [o for o, _ in done]
     with open(RESOURCES, "w") as f:
         json.dump([k for _, ks in done for k in ks], f, indent=0)
@@ -79,6 +114,7 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_module(module)
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB
