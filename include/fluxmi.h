@@ -652,8 +652,9 @@ fm_status_t fm_w4_pack(int64_t n_matrices, int64_t K, int64_t N, const uint8_t* 
 
 /*
  * fm_gemm_w4 -- fm_gemm with a 4-bit B, for few rows (a decode step):
- * C[M, N] = A[M, K] * W[K, N].  The weights are read once for every 32 rows;
+ * C[M, N] = A[M, K] * W[K, N].  The weights are read once for every 48 rows;
  * for hundreds of rows, unpacked 16-bit weights and fm_gemm are faster.
+ * C must not overlap A.
  *   ab      FM_F16 or FM_BF16: A and scales;  c  ab or FM_F32.
  *   packed  as above, 16-byte aligned; scales 16-byte aligned.
  * Codes enter the matrix cores exactly; products are summed in fp32 group by

@@ -178,7 +178,7 @@ def test_gate_extremes():
     ids, w, c, s, loss = _forward(x, 3, score=0)
     assert ids[1].tolist() == [0, 1, 3]       # a NaN is never chosen
     assert torch.isnan(s).all() and torch.isnan(loss).all()
-    mask = torch.zeros(4, dtype=torch.uint8, device="cuda:0")
+    mask = torch.zeros(4, dtype=torch.bool, device="cuda:0")     # bool holds the same bytes
     ids, w, c, s, loss = _forward(x, 2, token_mask=mask)
     assert (ids == -1).all() and (w == 0).all() and (c == 0).all() and (s == 0).all()
     assert loss.item() == 0

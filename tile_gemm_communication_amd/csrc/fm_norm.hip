@@ -10,13 +10,16 @@
 namespace fm {
 namespace {
 
+constexpr int64_t kNormGridX = 1 << 20;
+
 // TH lanes hold a row; a block of 256 has 4 rows of 64 lanes, else one row.
 template <typename E, typename S, typename B, int TH, int CH>
 __global__ __launch_bounds__(TH == 64 ? 256 : TH) void norm_fwd(const NormArgs a) {
   constexpr int RW = TH == 64 ? 4 : 1;
   __shared__ float s_red[2][TH / 64];
   const int t = threadIdx.x % TH, N = a.N;
-  const int64_t row = (int64_t)blockIdx.x * RW + threadIdx.x / TH;
+  const int64_t row =
+      ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RW + threadIdx.x / TH;
   if (row >= a.M) return;   // whole waves, and RW > 1 has no barrier
   const float invN = 1.f / (float)N;
 
@@ -74,9 +77,13 @@ __global__ __launch_bounds__(TH == 64 ? 256 : TH) void norm_fwd(const NormArgs a
 
 template <typename E, typename S, typename B>
 void launch_fwd(const NormArgs& a, hipStream_t stream) {
+// two grid dimensions: one holds fewer than 2^32 lanes
 #define FM_FWD(TH, CH)                                                                       \
-  hipLaunchKernelGGL((norm_fwd<E, S, B, TH, CH>), dim3(cdiv(a.M, TH == 64 ? 4 : 1)),         \
-                     dim3(TH == 64 ? 256 : TH), 0, stream, a)
+  do {                                                                                       \
+    const int64_t blocks = cdiv(a.M, TH == 64 ? 4 : 1), x = blocks < kNormGridX ? blocks : kNormGridX; \
+    hipLaunchKernelGGL((norm_fwd<E, S, B, TH, CH>), dim3((unsigned)x, (unsigned)cdiv(blocks, x)), \
+                       dim3(TH == 64 ? 256 : TH), 0, stream, a);                             \
+  } while (0)
   const int N = a.N;
   if (N <= 256) FM_FWD(64, 1);
   else if (N <= 512) FM_FWD(64, 2);
@@ -111,7 +118,8 @@ fm_status_t check_norm(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t block_dt,
   if (M < 0 || N < 0 || N % 8) return FM_ERR_INVALID_ARG;
   if (gate ? (n_gates < 1 || (M > 0 && (n_gates > M || M % n_gates))) : n_gates != 0)
     return FM_ERR_INVALID_ARG;
-  if (N > kNormMaxN || M >= (1ll << 31)) return FM_ERR_UNSUPPORTED;
+  if (N > kNormMaxN || M >= (1ll << 31) || (M == 0 && n_gates > kNormGridX))
+    return FM_ERR_UNSUPPORTED;
   return FM_OK;
 }
 

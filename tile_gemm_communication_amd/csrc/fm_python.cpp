@@ -61,6 +61,12 @@ struct Call {
     return t->data_ptr();
   }
 
+  // A token mask: uint8, or bool, which holds the same bytes.
+  void* mask(PyObject* o, int64_t T) {
+    const at::Tensor* t = tensor("token_mask", o);
+    return at("token_mask", o, t && t->scalar_type() == at::kBool ? at::kBool : at::kByte, {T});
+  }
+
   // A workspace of any type.
   void* workspace(PyObject* o, size_t& bytes) {
     bytes = 0;
@@ -131,7 +137,7 @@ PyObject* moe_gate(PyObject*, PyObject* const* v, Py_ssize_t n) {
   void* ws = c.workspace(v[13], bytes);
   void *px = c.at("logits", v[2], dt, {T, E}), *pid = c.at("topk_ids", v[3], kInt, {T, topk}),
        *pw = c.at("topk_weights", v[4], kFloat, {T, topk}), *pb = c.at("bias", v[8], kFloat, {E}),
-       *pm = c.at("token_mask", v[9], kByte, {T}), *pc = c.at("counts", v[10], kInt, {E + 1}),
+       *pm = c.mask(v[9], T), *pc = c.at("counts", v[10], kInt, {E + 1}),
        *ps = c.at("prob_sums", v[11], kFloat, {E}), *pl = c.at("loss", v[12], kFloat, {1});
   const int64_t score = a.i(5), renorm = a.i(6);
   const float scale = a.f(7);
@@ -155,7 +161,7 @@ PyObject* moe_gate_bwd(PyObject*, PyObject* const* v, Py_ssize_t n) {
   const at::ScalarType dt = x->scalar_type();
   const fm_dtype_t code = c.code(dt);
   void *px = c.at("logits", v[2], dt, {T, E}), *pid = c.at("topk_ids", v[3], kInt, {T, topk}),
-       *pd = c.at("d_logits", v[4], dt, {T, E}), *pm = c.at("token_mask", v[8], kByte, {T}),
+       *pd = c.at("d_logits", v[4], dt, {T, E}), *pm = c.mask(v[8], T),
        *pw = c.at("d_weights", v[9], kFloat, {T, topk}), *pc = c.at("counts", v[10], kInt, {E + 1}),
        *pl = c.at("d_loss", v[11], kFloat, {1});
   const int64_t score = a.i(5), renorm = a.i(6);
