@@ -398,9 +398,10 @@ __device__ __forceinline__ float four_row_step(const W4Consts<E>& k, u32x4& w,
   return acc;
 }
 
-// A block owns up to a.tiles tiles of 16 columns and its 8 waves share K in
-// contiguous parts; a wave streams through its part of one tile after another
-// without a stop between them.  x lies in LDS, so that the loads in flight are
+// A block owns a.tiles tiles of 16 columns (1, 2, 4 or 8); its 8 waves share the
+// tiles, and K in contiguous parts where they outnumber them (each of the tiles'
+// parts on all 8 waves instead, one tile after another: 61 pairs of 64 experts,
+// 4096 x 2816, 87 us for 79).  x lies in LDS, so that the loads in flight are
 // weights and scales alone (memory loads complete in order: an x load behind them
 // would wait for them).
 constexpr int kAhead = 2;   // steps of 128 k in flight; 3 and 4 measured no better, 6 worse
@@ -412,9 +413,9 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
   constexpr int PF = kAhead, XB = 3, GP = 4 / GB;
   __shared__ int s_rows[ROUTE ? kW4Threads : 1];   // the expert's pairs
   __shared__ __align__(16) char s_own[R > 1 ? kW4Waves * 1024 : 16];
-  extern __shared__ __align__(16) char s_dyn[];    // [tiles][waves][R][16] sums, then x
-  float* s_part = reinterpret_cast<float*>(s_dyn);
-  const W4Stage st = stage_at(s_dyn + a.tiles * (kW4Waves * R * 64), a.blocks, R);
+  __shared__ float s_part[kW4Waves][R * 16];
+  extern __shared__ __align__(16) char s_dyn[];    // x
+  const W4Stage st = stage_at(s_dyn, a.blocks, R);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = threadIdx.x >> 2 & 15, q = threadIdx.x & 3;
   const int sc16 = R > 1 ? threadIdx.x & 15 : c16;   // the column whose sums the lane takes
@@ -436,9 +437,13 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
   }
   const W4Source src = source_of<Z>(a, e, n0, 16 * a.tiles);
   const uint32_t wo = (uint32_t)c16 * a.blocks * 64 + q * 16;   // columns past N read 0
-  const int per = (a.blocks + kW4Waves - 1) / kW4Waves;
-  const int s0 = min(a.blocks, wave * per), steps = min(a.blocks, s0 + per) - s0;
-  const int tiles = min(a.tiles, (a.N - n0 + 15) >> 4), total = steps * tiles;
+  // Tiles and the parts of K are powers of two.
+  const int shift = 3 - __builtin_ctz(a.tiles), parts = 1 << shift;
+  const int tile = wave >> shift;
+  const bool busy = n0 + tile * 16 < a.N;
+  const int per = (a.blocks + parts - 1) >> shift;
+  const int s0 = busy ? min(a.blocks, (wave & parts - 1) * per) : 0;
+  const int steps = busy ? min(a.blocks, s0 + per) - s0 : 0;
   const W4Consts<E> consts;
 
   for (int64_t m0 = MODE <= kDense32 ? (int64_t)blockIdx.z * R : 0; m0 < rows;
@@ -484,20 +489,19 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
 
     u32x4 w[PF];
     W4Scales<E, GB, Z> sc[PF];
-    // Where the wave's next step lies in the resources (bytes, scalar): its part of K
-    // of one tile after another; past the last step, anywhere inside.
-    const int w_last = steps ? ((tiles - 1) * 16 * a.blocks + s0 + steps - 1) * 64 : 0;
-    const int s_last = ((a.groups - 1) * a.N + n0 + (tiles - 1) * 16) * 2 * a.some;
+    // Where the wave's next step lies in the resources (bytes, scalar); past the last
+    // step, that one again.
+    const int at0 = busy ? tile * 16 : 0;   // the wave's first column of the block's
+    const int w_last = (at0 * a.blocks + max(s0 + steps - 1, 0)) * 64;
+    const int s_last = ((a.groups - 1) * a.N + n0 + at0) * 2 * a.some;
     const int s_step = a.N * (2 * GP);
-    const int w_turn = (16 * a.blocks + 1 - steps) * 64, s_turn = 32 - (steps - 1) * s_step;
-    int li = 0, lw = min(s0 * 64, w_last), ls = min((s0 * GP * a.N + n0) * 2 * a.some, s_last);
+    int lw = min((at0 * a.blocks + s0) * 64, w_last);
+    int ls = min((s0 * GP * a.N + n0 + at0) * 2 * a.some, s_last);
     auto load = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
       wr = load_codes(src, wo, lw);
       load_scales<E, GB, Z>(sr, src, sc16, ls, a.N * 2, s_last);
-      const bool turn = ++li == steps;
-      lw = min(lw + (turn ? w_turn : 64), w_last);
-      ls = min(ls + (turn ? s_turn : s_step), s_last);
-      li = turn ? 0 : li;
+      lw = min(lw + 64, w_last);
+      ls = min(ls + s_step, s_last);
     };
     // Every load up to here is issued by all waves on one path, needed or not (none
     // leaves its resource): behind a branch the compiler would wait for them early.
@@ -515,10 +519,9 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
     __syncthreads();
     static_assert(R == 1 || R == 4, "one row, or four");
     float acc = 0.f;
-    int step = s0, left = steps;   // of the tile in use
+    int step = s0;
     const int i4 = threadIdx.x >> 2 & 3, k4 = threadIdx.x >> 4 & 3;
     const int x_row = i4 < count ? i4 : 0, sum_row = k4 < count ? k4 : 0;
-    float* sum = s_part + wave * R * 16 + (R > 1 ? threadIdx.x & 63 : c16);
     auto use = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
       if constexpr (R == 1)
         acc += one_row_step<E, GB, Z>(consts, wr, sr, st, step);
@@ -526,41 +529,31 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
         acc += four_row_step<E, GB, Z>(consts, wr, sr, st, step, x_row, sum_row,
                                        s_own + wave * 1024);
       ++step;
-      if (--left == 0) {
-        if constexpr (R == 1) acc = group_sum<4>(acc);
-        if (R > 1 || q == 0) *sum = acc;
-        acc = 0.f;
-        sum += kW4Waves * R * 16;
-        step = s0;
-        left = steps;
-      }
       __builtin_amdgcn_sched_barrier(0);   // a load kept behind the use needs no other registers
     };
     // No copy of the body for the last steps: the first pass over the code waits for
     // its instructions too.
 #pragma clang loop unroll(disable)
-    for (int i = 0; i < total; i += PF) {
+    for (int i = 0; i < steps; i += PF) {
 #pragma unroll
       for (int p = 0; p < PF; ++p) {
-        if (i + p < total) use(w[p], sc[p]);
+        if (i + p < steps) use(w[p], sc[p]);
         load(w[p], sc[p]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    // Opaque, so that what follows from it is not held in registers all along.
-    int t = threadIdx.x;
-    asm volatile("" : "+v"(t));
-    if (steps == 0)
-      for (int o = t & 63; o < tiles * R * 16; o += 64)
-        s_part[((o / (R * 16)) * kW4Waves + wave) * R * 16 + o % (R * 16)] = 0.f;
+    if constexpr (R == 1) acc = group_sum<4>(acc);
+    if (R > 1 || q == 0) s_part[wave][R > 1 ? threadIdx.x & 63 : c16] = acc;
     __syncthreads();
-    for (int o = t; o < tiles * R * 16; o += kW4Threads) {
-      const int tile = o / (R * 16), m = (o >> 4) % R, col = n0 + tile * 16 + (o & 15);
+    for (int o = threadIdx.x; o < a.tiles * R * 16; o += kW4Threads) {
+      const int t = o / (R * 16), m = (o >> 4) % R, col = n0 + t * 16 + (o & 15);
       if (m < count && col < a.N) {
         float v = 0.f;
 #pragma unroll
-        for (int u = 0; u < kW4Waves; ++u)
-          v += s_part[(tile * kW4Waves + u) * R * 16 + o % (R * 16)];
+        for (int u = 0; u < kW4Waves; ++u) {
+          const float p = s_part[(t << shift) + u & kW4Waves - 1][o % (R * 16)];
+          v += u < parts ? p : 0.f;
+        }
         store_out<E, MODE>(a, first, m0 + m, col, v);
       }
     }
@@ -893,11 +886,10 @@ __global__ __launch_bounds__(256) void w4_pack(int64_t n_matrices, int64_t K, in
 
 constexpr int64_t kFewLds = 128 << 10;   // most LDS that x may take
 
-// Column tiles of a block: one until there are blocks enough to fill the chip a
-// few times over, then up to 8, which spread a block's fixed costs (4096 x 2816,
-// 61 tokens over 64 experts: 1 tile 160 us, 2 119, 4 110, 8 108; 8 experts: 1 tile
-// 22.7 us, 2 21.5, 4 23).
-constexpr int64_t kFewBlocks = 1024;
+// Column tiles of a block: one until there are blocks enough to fill the chip twice
+// over, then up to 8, which spread a block's fixed costs (4096 x 2816, 61 tokens: 8
+// experts, 1 tile 16.3 us, 2 14.0, 4 15.7; 64 experts, 2 tiles 89 us, 4 83, 8 80).
+constexpr int64_t kFewBlocks = 512;
 int few_tiles(int64_t blocks) {
   int t = 1;
   while (t < 8 && blocks / (2 * t) >= kFewBlocks) t *= 2;
@@ -912,7 +904,7 @@ void launch_rows(W4Args a, int64_t most, dim3 grid, hipStream_t stream) {
     a.tiles = few_tiles((int64_t)grid.x * grid.y * grid.z);                                  \
     grid.x = (unsigned)cdiv(a.N, 16 * a.tiles);                                              \
     hipLaunchKernelGGL((w4_few<E, GB, Z, R, MODE, ROUTE>), grid, dim3(kW4Threads),           \
-                       stage_bytes(a.blocks, R) + a.tiles * (kW4Waves * R * 64), stream, a); \
+                       stage_bytes(a.blocks, R), stream, a);                                 \
   } while (0)
 #define FM_MANY(MT, NT)                                                                      \
   do {                                                                                       \
