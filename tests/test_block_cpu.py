@@ -247,6 +247,15 @@ def test_pack_refusals_and_sizes():
     assert fm.fm_norm_residual_workspace_bytes(16, 64, 4) > 0
 
 
+def test_token_counts_past_every_index():
+    """Products of such a T wrap round; the counts themselves are refused."""
+    T = 1 << 61
+    assert gate_call(T=T, topk=16) == UNS and gate_bwd_call(T=T, topk=16) == UNS
+    assert gather_w4_call(T=T) == UNS and scatter_w4_call(T=T, topk=8) == UNS
+    assert fm.fm_moe_gate_workspace_bytes(T, 64) == 0
+    assert fm.fm_moe_w4_workspace_bytes(T, 8, 64) == 0
+
+
 def _native():
     pytest.importorskip("torch")
     fm.lib()

@@ -622,7 +622,7 @@ fm_status_t check_gate(fm_dtype_t dt, int64_t T, int E, int topk, int score, int
     return FM_ERR_INVALID_ARG;
   if ((score != FM_GATE_SOFTMAX && score != FM_GATE_SIGMOID) || renorm < 0 || renorm > 1)
     return FM_ERR_INVALID_ARG;
-  if (T * topk >= (1ll << 31)) return FM_ERR_UNSUPPORTED;
+  if (T >= (1ll << 31) || T * topk >= (1ll << 31)) return FM_ERR_UNSUPPORTED;
   if (T > 0 && (!logits || !aligned16(logits))) return FM_ERR_INVALID_ARG;
   return FM_OK;
 }
@@ -645,7 +645,7 @@ using namespace fm;
   }
 
 extern "C" size_t fm_moe_gate_workspace_bytes(int64_t T, int32_t n_experts) {
-  if (T < 0 || n_experts < 1 || n_experts > kGateMaxExperts) return 0;
+  if (T < 0 || T >= (1ll << 31) || n_experts < 1 || n_experts > kGateMaxExperts) return 0;
   return gate_ws(T, n_experts);
 }
 

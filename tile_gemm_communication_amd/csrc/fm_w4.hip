@@ -1045,7 +1045,8 @@ extern "C" fm_status_t fm_moe_gather_gemm_w4(
   fm_status_t st = check_w4(dt, ffn, hidden, group, X, packed, scales, T > 0 && ffn > 0);
   if (st != FM_OK) return st;
   if (T > 0 && ffn > 0 && (!H || !aligned16(H))) return FM_ERR_INVALID_ARG;
-  if (T > 0 && T * hidden * 2 >= kNoX) return FM_ERR_UNSUPPORTED;   // 32-bit row offsets
+  if (T >= (1ll << 31) || (T > 0 && T * hidden * 2 >= kNoX))
+    return FM_ERR_UNSUPPORTED;   // 32-bit row offsets
   // A decode step's pairs are sorted by the product's own blocks (one launch); more
   // pairs, or rows too long for LDS, by the route's.
   const int64_t pairs = T * topk;
@@ -1090,6 +1091,7 @@ extern "C" fm_status_t fm_moe_gather_gemm_w4(
 
 extern "C" size_t fm_moe_w4_workspace_bytes(int64_t T, int32_t topk, int64_t hidden) {
   if (T < 0 || topk < 1 || hidden < 0 || hidden % 8) return 0;
+  if (T >= (1ll << 31) || T * topk >= (1ll << 31) || hidden >= (1ll << 22)) return 0;
   return (size_t)std::max<int64_t>(T * topk * hidden * 4, 256);
 }
 
@@ -1102,7 +1104,7 @@ extern "C" fm_status_t fm_moe_gemm_scatter_w4(
   const fm_status_t st = check_w4(dt, hidden, ffn, group, H, packed, scales, T > 0 && hidden > 0);
   if (st != FM_OK) return st;
   if (T < 0 || topk < 1 || n_local < 1 || n_local > kW4MaxExperts) return FM_ERR_INVALID_ARG;
-  if (T * topk >= (1ll << 31)) return FM_ERR_UNSUPPORTED;
+  if (T >= (1ll << 31) || T * topk >= (1ll << 31)) return FM_ERR_UNSUPPORTED;
   if (T == 0 || hidden == 0) return FM_OK;
   if (!topk_ids || !sorted_pairs || !expert_offsets || !topk_weights || !out || !aligned16(out) ||
       !aligned16(add) || !ws || !aligned16(ws) ||
