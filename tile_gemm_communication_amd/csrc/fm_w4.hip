@@ -22,7 +22,8 @@ constexpr int kW4Threads = 64 * kW4Waves;
 constexpr int kManyWaves = 8;            // more rows
 constexpr int kManyThreads = 64 * kManyWaves;
 constexpr int kW4MaxExperts = 64;
-constexpr int64_t kFewRows = 16;   // mean rows of an expert up to which x goes through LDS
+constexpr int64_t kMixedRows = 16;   // mean rows of an expert up to which w4_mixed runs
+constexpr int kFewRows = 4;          // rows of an expert up to which all of them lie in LDS
 
 __device__ __forceinline__ f32x4 mfma16(F16, u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
@@ -257,9 +258,18 @@ __device__ __forceinline__ W4Expert route_here(const W4Args& a, int* s_rows, int
   return x;
 }
 
-template <W4Mode MODE>
-__device__ __forceinline__ int64_t x_row(const W4Args& a, int64_t first, int64_t m) {
-  return MODE == kGather ? a.pairs[first + m] / a.topk : first + m;
+// What a block works on: the columns from n0 of one matrix, and the rows that it
+// multiplies, which s_rows lists where the block routed them itself.
+struct W4Work {
+  int n0, e;
+  int64_t first, rows;
+  const int* s_rows;
+};
+
+template <W4Mode MODE, bool ROUTE>
+__device__ __forceinline__ int64_t x_row(const W4Args& a, const W4Work& b, int64_t m) {
+  if (MODE != kGather) return b.first + m;
+  return (ROUTE ? b.s_rows[m] : a.pairs[b.first + m]) / a.topk;
 }
 
 // Stores output (row m of the expert's, col) = v.
@@ -406,35 +416,23 @@ __device__ __forceinline__ float four_row_step(const W4Consts<E>& k, u32x4& w,
 // would wait for them).
 constexpr int kAhead = 2;   // steps of 128 k in flight; 3 and 4 measured no better, 6 worse
 
+// LDS: x, then the waves' own memory and their sums.
+__host__ __device__ constexpr int few_own(int R) { return R > 1 ? kW4Waves * 1024 : 0; }
+__host__ __device__ inline int64_t few_lds(int blocks, int R) {
+  return stage_bytes(blocks, R) + few_own(R) + kW4Waves * R * 64;
+}
+
 template <typename E, int GB, bool Z, int R, W4Mode MODE, bool ROUTE>
-__global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_few(
-    const W4Args a) {
-  typedef typename Elem<E>::type L;
+__device__ __forceinline__ void few_rows(const W4Args& a, const W4Work& b, char* lds) {
   constexpr int PF = kAhead, XB = 3, GP = 4 / GB;
-  __shared__ int s_rows[ROUTE ? kW4Threads : 1];   // the expert's pairs
-  __shared__ __align__(16) char s_own[R > 1 ? kW4Waves * 1024 : 16];
-  __shared__ float s_part[kW4Waves][R * 16];
-  extern __shared__ __align__(16) char s_dyn[];    // x
-  const W4Stage st = stage_at(s_dyn, a.blocks, R);
+  const W4Stage st = stage_at(lds, a.blocks, R);
+  char* s_own = lds + stage_bytes(a.blocks, R);
+  float* s_part = reinterpret_cast<float*>(s_own + few_own(R));   // [waves][R * 16]
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = threadIdx.x >> 2 & 15, q = threadIdx.x & 3;
   const int sc16 = R > 1 ? threadIdx.x & 15 : c16;   // the column whose sums the lane takes
-  const int n0 = column_tile() * 16 * a.tiles;
-  int e = 0;
-  int64_t first = 0, rows = a.M;
-  if (MODE == kGather || MODE == kScatter) {
-    W4Expert x;
-    if constexpr (ROUTE) {
-      __shared__ int s_count[kW4MaxExperts], s_wave[kW4Waves];
-      x = route_here(a, s_rows, s_count, s_wave);
-    } else {
-      x = find_expert(a);
-    }
-    if (x.rows <= 0) return;
-    e = x.e;
-    first = x.first;
-    rows = x.rows;
-  }
+  const int n0 = b.n0, e = b.e;
+  const int64_t first = b.first, rows = b.rows;
   const W4Source src = source_of<Z>(a, e, n0, 16 * a.tiles);
   const uint32_t wo = (uint32_t)c16 * a.blocks * 64 + q * 16;   // columns past N read 0
   // Tiles and the parts of K are powers of two.
@@ -467,8 +465,7 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
     auto fetch = [&](const Piece& p) {
       int row = min(p.m, count - 1);   // rows past the last repeat it
       if (MODE == kGather)
-        row = ROUTE ? __builtin_amdgcn_readfirstlane(s_rows[m0 + row]) / a.topk
-                    : (int)x_row<MODE>(a, first, m0 + row);
+        row = __builtin_amdgcn_readfirstlane((int)x_row<MODE, ROUTE>(a, b, m0 + row));
       const bool in = lane_x + p.c * (kW4Threads * 16) < (uint32_t)a.K * 2;
       return __builtin_bit_cast(
           u32x4, __builtin_amdgcn_raw_buffer_load_b128(
@@ -543,7 +540,7 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
       }
     }
     if constexpr (R == 1) acc = group_sum<4>(acc);
-    if (R > 1 || q == 0) s_part[wave][R > 1 ? threadIdx.x & 63 : c16] = acc;
+    if (R > 1 || q == 0) s_part[wave * R * 16 + (R > 1 ? threadIdx.x & 63 : c16)] = acc;
     __syncthreads();
     for (int o = threadIdx.x; o < a.tiles * R * 16; o += kW4Threads) {
       const int t = o / (R * 16), m = (o >> 4) % R, col = n0 + t * 16 + (o & 15);
@@ -551,7 +548,7 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
         float v = 0.f;
 #pragma unroll
         for (int u = 0; u < kW4Waves; ++u) {
-          const float p = s_part[(t << shift) + u & kW4Waves - 1][o % (R * 16)];
+          const float p = s_part[((t << shift) + u & kW4Waves - 1) * R * 16 + o % (R * 16)];
           v += u < parts ? p : 0.f;
         }
         store_out<E, MODE>(a, first, m0 + m, col, v);
@@ -571,23 +568,14 @@ constexpr int many_lds(int MT, int NT) {
   return kManyWaves * (MT * 16 * kManyRow + NT * 1024);
 }
 
-template <typename E, int GB, bool Z, int MT, int NT, W4Mode MODE>
-__global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
+template <typename E, int GB, bool Z, int MT, int NT, W4Mode MODE, bool ROUTE>
+__device__ __forceinline__ void many_rows(const W4Args& a, const W4Work& b, char* s_dyn) {
   constexpr int ROWS = 16 * MT, GP = 4 / GB, XL = MT * 4;   // loads of 4 rows
-  extern __shared__ __align__(16) char s_dyn[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, q = lane >> 4;
-  const int n0 = column_tile() * 16 * NT;
-  int e = 0;
-  int64_t first = 0, rows = a.M;
-  if (MODE == kGather || MODE == kScatter) {
-    const W4Expert x = find_expert(a);
-    if (x.rows <= 0) return;
-    e = x.e;
-    first = x.first;
-    rows = x.rows;
-  }
+  const int n0 = b.n0, e = b.e;
+  const int64_t first = b.first, rows = b.rows;
   char* own_x = s_dyn + wave * (MT * 16 * kManyRow + NT * 1024);
   char* own_w = own_x + MT * 16 * kManyRow;
   const W4Source src = source_of<Z>(a, e, n0, 16 * NT);
@@ -609,7 +597,7 @@ __global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
     uint32_t xo[XL];   // lane: row lane / 16 of four, 16 bytes lane % 16 of a step's 256
 #pragma unroll
     for (int i = 0; i < XL; ++i)   // rows past the last repeat it
-      xo[i] = (uint32_t)(x_row<MODE>(a, first, min(m0 + i * 4 + q, rows - 1)) - from) * a.K * 2 +
+      xo[i] = (uint32_t)(x_row<MODE, ROUTE>(a, b, min(m0 + i * 4 + q, rows - 1)) - from) * a.K * 2 +
               i16 * 16;
     u32x4 w[NT], x[XL];
     W4Scales<E, GB, Z> sc[NT], now[NT];
@@ -717,6 +705,59 @@ __global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
     }
     __syncthreads();
   }
+}
+
+// The rows of this block's expert, or of a dense product; false past the last expert.
+template <W4Mode MODE, bool ROUTE>
+__device__ __forceinline__ bool find_work(const W4Args& a, int columns, W4Work& b) {
+  b = {column_tile() * columns, 0, 0, a.M, nullptr};
+  if (MODE == kGather || MODE == kScatter) {
+    W4Expert x;
+    if constexpr (ROUTE) {
+      __shared__ int s_rows[kW4Threads];   // the expert's pairs
+      __shared__ int s_count[kW4MaxExperts], s_wave[kW4Waves];
+      x = route_here(a, s_rows, s_count, s_wave);
+      b.s_rows = s_rows;
+    } else {
+      x = find_expert(a);
+    }
+    b.e = x.e;
+    b.first = x.first;
+    b.rows = x.rows;
+  }
+  return b.rows > 0;
+}
+
+// One row.
+template <typename E, int GB, bool Z, W4Mode MODE, bool ROUTE>
+__global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_one(
+    const W4Args a) {
+  extern __shared__ __align__(16) char s_dyn[];
+  W4Work b;
+  if (find_work<MODE, ROUTE>(a, 16 * a.tiles, b))
+    few_rows<E, GB, Z, 1, MODE, ROUTE>(a, b, s_dyn);
+}
+
+// Experts of few rows, as each block finds them: the host knows the mean at most.
+template <typename E, int GB, bool Z, W4Mode MODE, bool ROUTE>
+__global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_mixed(
+    const W4Args a) {
+  extern __shared__ __align__(16) char s_dyn[];
+  W4Work b;
+  if (!find_work<MODE, ROUTE>(a, 16 * a.tiles, b)) return;
+  if (b.rows <= kFewRows || a.tiles < 2) {
+    few_rows<E, GB, Z, 4, MODE, ROUTE>(a, b, s_dyn);
+  } else {
+    for (const int end = min(b.n0 + 16 * a.tiles, a.N); b.n0 < end; b.n0 += 32)
+      many_rows<E, GB, Z, 1, 2, MODE, ROUTE>(a, b, s_dyn);
+  }
+}
+
+template <typename E, int GB, bool Z, int MT, int NT, W4Mode MODE>
+__global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
+  extern __shared__ __align__(16) char s_dyn[];
+  W4Work b;
+  if (find_work<MODE, false>(a, 16 * NT, b)) many_rows<E, GB, Z, MT, NT, MODE, false>(a, b, s_dyn);
 }
 
 // The second layer of a single token's few pairs (at most kTinyPairs): a block
@@ -898,14 +939,6 @@ int few_tiles(int64_t blocks) {
 
 template <typename E, int GB, bool Z, W4Mode MODE>
 void launch_rows(W4Args a, int64_t most, dim3 grid, hipStream_t stream) {
-#define FM_FEW(R, ROUTE)                                                                     \
-  do {                                                                                       \
-    if (MODE <= kDense32) grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, R), 65535);         \
-    a.tiles = few_tiles((int64_t)grid.x * grid.y * grid.z);                                  \
-    grid.x = (unsigned)cdiv(a.N, 16 * a.tiles);                                              \
-    hipLaunchKernelGGL((w4_few<E, GB, Z, R, MODE, ROUTE>), grid, dim3(kW4Threads),           \
-                       stage_bytes(a.blocks, R), stream, a);                                 \
-  } while (0)
 #define FM_MANY(MT, NT)                                                                      \
   do {                                                                                       \
     if (MODE <= kDense32) grid.z = (unsigned)std::min<int64_t>(cdiv(a.M, 16 * MT), 65535);   \
@@ -913,21 +946,29 @@ void launch_rows(W4Args a, int64_t most, dim3 grid, hipStream_t stream) {
     hipLaunchKernelGGL((w4_many<E, GB, Z, MT, NT, MODE>), grid, dim3(kManyThreads),          \
                        many_lds(MT, NT), stream, a);                                         \
   } while (0)
-  if constexpr (MODE == kGather) {
-    if (a.n_pairs > 0) {
-      if (most == 1) FM_FEW(1, true);
-      else FM_FEW(4, true);
+  constexpr bool ROUTE = MODE == kGather;   // there, only where the blocks route
+  a.tiles = few_tiles((int64_t)grid.x * grid.y);
+  const dim3 few((unsigned)cdiv(a.N, 16 * a.tiles), grid.y);
+  if constexpr (MODE != kScatter) {
+    if ((ROUTE ? a.n_pairs : a.M) == 1 && stage_bytes(a.blocks, 1) <= kFewLds) {
+      hipLaunchKernelGGL((w4_one<E, GB, Z, MODE, ROUTE>), few, dim3(kW4Threads),
+                         few_lds(a.blocks, 1), stream, a);
       return;
     }
   }
-  if ((most == 1 || (most <= 8 && stage_bytes(a.blocks, 4) > kFewLds)) &&
-      stage_bytes(a.blocks, 1) <= kFewLds)
-    FM_FEW(1, false);
-  else if (most <= 8 && stage_bytes(a.blocks, 4) <= kFewLds) FM_FEW(4, false);
-  else if (most <= 16) FM_MANY(1, 2);
+  if constexpr (MODE == kGather || MODE == kScatter) {
+    if (ROUTE ? a.n_pairs > 0
+              : most <= 2 * kMixedRows && stage_bytes(a.blocks, 4) <= kFewLds) {
+      if (most > 2 * kFewRows) a.tiles = std::max(a.tiles, 2);
+      hipLaunchKernelGGL((w4_mixed<E, GB, Z, MODE, ROUTE>),
+                         dim3((unsigned)cdiv(a.N, 16 * a.tiles), grid.y), dim3(kW4Threads),
+                         std::max<int64_t>(few_lds(a.blocks, 4), many_lds(1, 2)), stream, a);
+      return;
+    }
+  }
+  if (most <= 16) FM_MANY(1, 2);
   else if (most <= 32) FM_MANY(2, 2);
   else FM_MANY(3, 3);
-#undef FM_FEW
 #undef FM_MANY
 }
 
@@ -1051,7 +1092,7 @@ extern "C" fm_status_t fm_moe_gather_gemm_w4(
   // pairs, or rows too long for LDS, by the route's.
   const int64_t pairs = T * topk;
   const bool here = T > 0 && ffn > 0 && topk > 0 && T <= kW4Threads && pairs <= kW4Threads &&
-                    n_local >= 1 && n_local <= kW4MaxExperts && pairs / n_local <= kFewRows &&
+                    n_local >= 1 && n_local <= kW4MaxExperts && pairs / n_local <= kMixedRows &&
                     hidden <= 4 * kFewLds && stage_bytes((int)cdiv(hidden, 128), 4) <= kFewLds;
   if (here) {
     st = check_route(T, topk, n_local, topk_ids, sorted_pairs, expert_offsets, ws, ws_bytes);
