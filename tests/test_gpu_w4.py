@@ -4,7 +4,9 @@ Tolerances, u = 2^-24.  A group's sums t = sum x (base + code) and S = sum x are
 exact products added in fp32: at most 32 additions in an instruction (2 u each, if it
 truncates) and 4 instructions, 72 u of sum |x| (base + 15).  scale, zero and the two
 fused multiply-adds add 4 u of the same; groups and waves are added up in chains of
-K / (32 * 8) and 8: (K / 256 + 8) u.  With base 16 (bf16) or 64 (fp16) and
+K / (32 * 8) and 8: (K / 256 + 8) u.  (Where the waves share several tiles the chains
+are up to K / 32 long, of terms within 15 sum |x| scale: up to K = 2185 that is within
+(K / 256 + 8) u of the magnitude below.)  With base 16 (bf16) or 64 (fp16) and
 |code - zero| <= 15 this is, for each output,
   (K / 256 + 84) u * 2 (base + 15) * sum_k |x_k| scale_k.
 Two roundings follow for a weight and the sum over k (topk u), each 16-bit output rounds
@@ -168,6 +170,9 @@ MOE = [  # T, hidden, ffn, E, nl, e0, topk, group, dt, zeros, act, closed (no to
     (9, 72, 20480, 8, 8, 0, 1, 128, "bf16", True, 2),
     (128, 136, 72, 64, 64, 0, 4, 64, "fp16", True, 3),     # 512 pairs: the most that one launch sorts
     (129, 136, 72, 64, 64, 0, 4, 64, "fp16", True, 3),
+    (100, 1288, 264, 64, 64, 0, 4, 32, "bf16", True, 3),   # 2 and 8 tiles a block; 1 to 12 rows
+    (61, 264, 520, 8, 8, 0, 2, 32, "bf16", False, 2),      # 8 to 22 rows
+    (61, 1288, 264, 64, 64, 0, 2, 128, "fp16", True, 0),
 ]
 
 

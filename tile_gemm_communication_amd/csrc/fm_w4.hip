@@ -1,15 +1,22 @@
 // fm_w4.hip -- products with 4-bit weights and group scales for few rows: the
 // dense shard, and the two matrices of each local expert of a MoE layer.
 //
-// With a handful of rows the weights are all there is to read, so the kernel is
-// built to stream them: a block owns 16 columns, its waves share K, and every
-// lane's 16-byte load is the B operand of four 16x16x32 matrix instructions.
+// With few rows the weights are all there is to read, so the kernels are built to
+// stream them in whole cache lines, two steps of 128 k ahead.  Three shapes:
+//   w4_one    one row: 4x4x4 products whose diagonal is what is wanted
+//   few_rows  up to 4 rows (experts): x in LDS, 4x4x4 products, a tile a wave
+//   many_rows 16, 32 or 48 rows at a time: 16x16x32 products, K over the waves
 // A code c enters the matrix core exactly, without a conversion, as the 16-bit
 // number base + c, whose bit pattern is the code shifted into a constant's
 // mantissa (bf16: base 16, fp16: base 64).  With t = sum x (base + c) and
 // S = sum x over one group of K (a matrix product with ones),
 //   sum x (c - zero) scale = scale * (t - (base + zero) * S),
 // so that scale and zero cost two fused multiply-adds a group and output.
+//
+// Measured (kernel alone; the bytes of codes, scales and zeros over that time):
+// 1 x 6144 x 12288 fp16 9.4 us (4.1 TB/s), 45 x 12288 x 6144 bf16 25 us (1.9 TB/s:
+// bound by x, which 128 blocks each read), 61 tokens over 8 of 64 experts of 4096 x
+// 2816 14.1 us (2.9 TB/s), over all 64 80 us (4.1 TB/s).
 #include <algorithm>
 
 #include "fm_wave.hpp"
@@ -22,8 +29,13 @@ constexpr int kW4Threads = 64 * kW4Waves;
 constexpr int kManyWaves = 8;            // more rows
 constexpr int kManyThreads = 64 * kManyWaves;
 constexpr int kW4MaxExperts = 64;
-constexpr int64_t kMixedRows = 16;   // mean rows of an expert up to which w4_mixed runs
-constexpr int kFewRows = 4;          // rows of an expert up to which all of them lie in LDS
+// Rows of an expert up to which they all lie in LDS (61 and 240 tokens over 64
+// experts, 4096 x 2816: 4 rows 79 and 115 us, 8 rows 82 and 127).
+constexpr int kFewRows = 4;
+// Mean rows of an expert up to which w4_mixed runs, with the route in its own blocks
+// for the first layer (8 experts, 4096 x 2816: 61 tokens 22.6 us, as two launches of
+// route and w4_many 31.5).
+constexpr int64_t kMixedRows = 16;
 
 __device__ __forceinline__ f32x4 mfma16(F16, u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
@@ -409,9 +421,8 @@ __device__ __forceinline__ float four_row_step(const W4Consts<E>& k, u32x4& w,
 }
 
 // A block owns a.tiles tiles of 16 columns (1, 2, 4 or 8); its 8 waves share the
-// tiles, and K in contiguous parts where they outnumber them (each of the tiles'
-// parts on all 8 waves instead, one tile after another: 61 pairs of 64 experts,
-// 4096 x 2816, 87 us for 79).  x lies in LDS, so that the loads in flight are
+// tiles, and K in contiguous parts where they outnumber them (with all 8 waves on
+// one tile after another, 61 tokens over 64 experts of 4096 x 2816 took 87 us for 80).  x lies in LDS, so that the loads in flight are
 // weights and scales alone (memory loads complete in order: an x load behind them
 // would wait for them).
 constexpr int kAhead = 2;   // steps of 128 k in flight; 3 and 4 measured no better, 6 worse
@@ -728,7 +739,7 @@ __device__ __forceinline__ bool find_work(const W4Args& a, int columns, W4Work& 
   return b.rows > 0;
 }
 
-// One row.
+// One row (6144 x 12288: 12.7 us a call, few_rows with 4 rows 16.7, many_rows 14.3).
 template <typename E, int GB, bool Z, W4Mode MODE, bool ROUTE>
 __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_one(
     const W4Args a) {
@@ -738,7 +749,8 @@ __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4)))
     few_rows<E, GB, Z, 1, MODE, ROUTE>(a, b, s_dyn);
 }
 
-// Experts of few rows, as each block finds them: the host knows the mean at most.
+// Experts of few rows, as each block finds them: the host knows a bound of the mean,
+// which on one rank of many is far above it.
 template <typename E, int GB, bool Z, W4Mode MODE, bool ROUTE>
 __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_mixed(
     const W4Args a) {
@@ -762,8 +774,10 @@ __global__ __launch_bounds__(kManyThreads) void w4_many(const W4Args a) {
 
 // The second layer of a single token's few pairs (at most kTinyPairs): a block
 // owns 16 columns of out and walks every local pair, its waves sharing K, so that
-// the weighted sum needs neither a second launch nor memory between.
-constexpr int kTinyPairs = 8;
+// the weighted sum needs neither a second launch nor memory between.  4096 x 2816,
+// this kernel and the two launches: 2 pairs 7.2 and 8.8 us, 4 pairs 11.1 and 10.3,
+// 8 pairs 20.3 and 14.4.
+constexpr int kTinyPairs = 3;
 
 struct W4TinyArgs {
   W4Args w;             // pairs, offsets: sorted_pairs, expert_offsets; ids, e0, n_pairs
@@ -966,6 +980,8 @@ void launch_rows(W4Args a, int64_t most, dim3 grid, hipStream_t stream) {
       return;
     }
   }
+  // Dense 6144 x 12288: 16 rows 16.7 us, with 32-row chunks 18.7; 32 rows 22.2 us,
+  // 16-row chunks 25.1, 48-row ones 28.6; 48 rows 31.1, 32-row chunks 32.9.
   if (most <= 16) FM_MANY(1, 2);
   else if (most <= 32) FM_MANY(2, 2);
   else FM_MANY(3, 3);
