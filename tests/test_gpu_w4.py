@@ -266,6 +266,37 @@ def test_scatter_w4(oracle, T, hidden, ffn, E, nl, e0, topk, group, dt, zeros, a
     assert torch.equal(inplace, outs[1])
 
 
+@pytest.mark.parametrize("T", [1, 3, 40, 600])
+def test_empty_contractions(T):
+    """Sums over nothing: zeros in C and in the local rows of H, add (or zeros) in out."""
+    import torch
+    say(f"w4 K=0 T={T}")
+    dev, bf = "cuda:0", torch.bfloat16
+    nl, topk, n = 4, 2, 200
+    x = torch.empty(T, 0, device=dev, dtype=bf)
+    c = torch.full((T, n), -7.0, device=dev)
+    fm.fm_gemm_w4(x, torch.empty(n, 0, dtype=torch.uint8, device=dev),
+                  torch.empty(0, n, dtype=bf, device=dev), c, 64)
+    assert (c == 0).all()
+    ids = _dev(np.stack([np.arange(T) % 8, np.arange(T) % 8 + 1], 1).astype(np.int32))   # some not local
+    local = int((ids < nl).sum())
+    p = torch.empty(nl, n, 0, dtype=torch.uint8, device=dev)
+    s = torch.empty(nl, 0, n, dtype=bf, device=dev)
+    h = torch.full((T * topk, n), -7.0, device=dev, dtype=bf)
+    sp = torch.full((T * topk,), -9, dtype=torch.int32, device=dev)
+    off = torch.zeros(nl + 1, dtype=torch.int32, device=dev)
+    fm.fm_moe_gather_gemm_w4(x, ids, p, s, h, sp, off, 0, 64, fm.moe_workspace(T, topk, n, nl))
+    assert int(off[-1]) == local and (h[:local] == 0).all() and (h[local:] == -7).all()
+    w = torch.ones(T, topk, device=dev)
+    add = torch.randn(T, n, device=dev)
+    ws = fm.moe_w4_workspace(T, topk, n)
+    he = torch.empty(T * topk, 0, device=dev, dtype=bf)
+    for given in (add, None):
+        out = torch.full((T, n), -7.0, device=dev)
+        fm.fm_moe_gemm_scatter_w4(he, p, s, ids, sp, off, w, out, 0, 64, ws, add=given)
+        assert torch.equal(out, add if given is not None else torch.zeros_like(add))
+
+
 def test_w4_agrees_with_the_16_bit_layer():
     """The same expert weights unpacked to 16 bits through the existing layer: codes and
     power-of-two scales are exact in bf16, so only the summation order differs."""

@@ -843,7 +843,7 @@ __global__ __launch_bounds__(kW4Threads) void w4_scatter_tiny(const W4TinyArgs a
     src = source_of<Z>(a, units ? __builtin_amdgcn_readlane(ex, at) : 0, n0, 16);
   };
 #pragma unroll
-  for (int p = 0; p < PF; ++p) {   // on one path and in the loop's order, as in w4_few
+  for (int p = 0; p < PF; ++p) {   // on one path and in the loop's order, as in few_rows
     load(w[p], sc[p]);
     __builtin_amdgcn_sched_barrier(0);
   }
