@@ -4,7 +4,8 @@
 // One row lies in the registers of TH lanes, CH chunks of four elements each, so
 // block and residual are read once and out and y written once: the operator is
 // bound by those bytes.  The two mean squares are the only exchanges between
-// lanes (DPP within a wave, one LDS slot a wave beyond).
+// lanes (DPP within a wave, one LDS slot a wave beyond).  16384 x 4096 bf16 with an
+// fp32 block: 133 us, 5.0 TB/s; 3 x 4096: 3.8 us, one wait for memory after another.
 #include "fm_norm.hpp"
 
 namespace fm {
@@ -77,7 +78,9 @@ __global__ __launch_bounds__(TH == 64 ? 256 : TH) void norm_fwd(const NormArgs a
 
 template <typename E, typename S, typename B>
 void launch_fwd(const NormArgs& a, hipStream_t stream) {
-// two grid dimensions: one holds fewer than 2^32 lanes
+// Lanes of a row, 16384 rows: N = 256 with 64 lanes 10.4 us, 256 20.3; 512 16.7 and
+// 23.9; 1024 either 31; 4096 with 256 lanes 127, 1024 133; 8192 with 1024 238, 256 321.
+// Two grid dimensions: one holds fewer than 2^32 lanes.
 #define FM_FWD(TH, CH)                                                                       \
   do {                                                                                       \
     const int64_t blocks = cdiv(a.M, TH == 64 ? 4 : 1), x = blocks < kNormGridX ? blocks : kNormGridX; \
