@@ -26,7 +26,9 @@ constexpr int kGateBwdWaves = kGateBwdThreads / 64;
 constexpr int64_t kGateBwdBlocks = 1024;
 constexpr int kGateMaxExperts = 1024;
 constexpr int kGateMaxTopk = 16;
-constexpr int kGateMaxBlocks = 256;     // blocks whose partial sums are joined
+// Blocks whose partial sums one block joins (65536 x 256: 256 blocks 72 us, 512 63, 1024
+// 78; 16384 x 256: 29, 34 and 34).
+constexpr int kGateMaxBlocks = 256;
 constexpr int kGateBatch = 18;          // loads in flight of the join: 256 blocks of 64 experts at once
 constexpr int kGateFinishThreads = 1024;
 constexpr float kNegInf = -__builtin_inff();

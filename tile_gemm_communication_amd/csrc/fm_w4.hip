@@ -16,7 +16,7 @@
 // Measured (kernel alone; the bytes of codes, scales and zeros over that time):
 // 1 x 6144 x 12288 fp16 9.4 us (4.1 TB/s), 45 x 12288 x 6144 bf16 25 us (1.9 TB/s:
 // bound by x, which 128 blocks each read), 61 tokens over 8 of 64 experts of 4096 x
-// 2816 14.1 us (2.9 TB/s), over all 64 80 us (4.1 TB/s).
+// 2816 14.1 us (3.0 TB/s), over all 64 80 us (4.1 TB/s).
 #include <algorithm>
 
 #include "fm_wave.hpp"
