@@ -173,6 +173,8 @@ MOE = [  # T, hidden, ffn, E, nl, e0, topk, group, dt, zeros, act, closed (no to
     (100, 1288, 264, 64, 64, 0, 4, 32, "bf16", True, 3),   # 2 and 8 tiles a block; 1 to 12 rows
     (61, 264, 520, 8, 8, 0, 2, 32, "bf16", False, 2),      # 8 to 22 rows
     (61, 1288, 264, 64, 64, 0, 2, 128, "fp16", True, 0),
+    (6, 12288, 72, 4, 4, 0, 2, 128, "bf16", False, 0),     # four rows nearly fill LDS
+    (6, 72, 12288, 4, 4, 0, 2, 64, "fp16", True, 0),
 ]
 
 
