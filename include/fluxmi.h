@@ -608,8 +608,10 @@ fm_status_t fm_norm_residual(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t blo
  *   d_y      [M, N] dt, gradient of y; NULL if and only if w_pre is.
  *   d_out    [M, N] stream_dt, gradient of out from its later uses, or NULL: 0.
  *   out      [M, N] stream_dt as the forward stored it; needed with w_pre.
- *   block    [M, N] block_dt; needed with w_post or d_gate.
- *   rstd_post, rstd_pre  as the forward stored them; needed with w_post, w_pre.
+ *   block    [M, N] block_dt; needed for d_gate, d_w_post and, with w_post, for
+ *            d_block.
+ *   rstd_post  as the forward stored it; needed where w_post is given and block
+ *            is needed.   rstd_pre  the same; needed with w_pre.
  *   d_resid  [M, N] stream_dt or NULL: gradient of resid (of out in total).
  *            It may be d_out itself.
  *   d_block  [M, N] block_dt or NULL.

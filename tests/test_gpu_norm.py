@@ -200,3 +200,38 @@ def test_norm_only_loss_gradient_of_out():
     ref, mag = ob.norm_bwd(_host(d_y), None, _host(v["resid"]), None, None, _host(v["w_pre"]), None,
                            1.0, None, _host(rp))
     assert (np.abs(_host(d) - ref["d_resid"]) <= 128 * U * mag["d_resid"] + 1e-38).all()
+
+
+@pytest.mark.parametrize("M,N,stream,block,G", [(5, 264, "fp32", "fp32", 0), (37, 4096, "bf16", "bf16", 1),
+                                                (6, 16384, "fp32", "bf16", 6), (300, 64, "bf16", "fp32", 100)])
+def test_norm_backward_of_a_frozen_block(M, N, stream, block, G):
+    """Where only d_resid and d_w_pre are wanted, w_post, gate and scale have no part: neither
+    block nor rstd_post has to be there, and the gradients are those of the call with both."""
+    import torch
+    say(f"norm bwd, frozen block M={M} N={N} {stream}/{block} G={G}")
+    v = _inputs(M, N, "bf16", stream, block, 1, 1, G, seed=4)
+    rng = np.random.default_rng(5)
+    d_y, d_out = _dev(rng.standard_normal((M, N)), "bf16"), _dev(rng.standard_normal((M, N)), stream)
+    rq = _dev(1 / np.sqrt((_host(v["block"]) ** 2).mean(1) + EPS), "fp32")
+    rp = _dev(1 / np.sqrt((_host(v["resid"]) ** 2).mean(1) + EPS), "fp32")
+    kw = dict(out=v["resid"], d_y=d_y, d_out=d_out, w_post=v["w_post"], w_pre=v["w_pre"], gate=v["gate"],
+              scale=0.7, rstd_pre=rp, ws=fm.norm_residual_workspace(M, N, G))
+    grads = []
+    for more, wanted in ((dict(block=v["block"], rstd_post=rq), "rp"), (dict(), "rp"), (dict(), "r"),
+                         (dict(), "p"), (dict(block=v["block"]), "rp")):
+        d = torch.full((M, N), -7.0, device="cuda:0", dtype=_dtype(stream)) if "r" in wanted else None
+        dp = torch.full((N,), -7.0, device="cuda:0") if "p" in wanted else None
+        fm.fm_norm_residual_bwd(d, None, **kw, **more, d_w_pre=dp)
+        torch.cuda.synchronize()
+        grads.append((d, dp))
+    ref, mag = ob.norm_bwd(*(_host(x) for x in (d_y, d_out, v["resid"], v["block"], v["w_post"],
+                                                v["w_pre"], v["gate"])), float(np.float32(0.7)),
+                           _host(rq), _host(rp))
+    for k, t, h, more in (("d_resid", grads[0][0], HALF[stream], 0), ("d_w_pre", grads[0][1], U, M / 256 + 80)):
+        err = np.abs(_host(t) - ref[k])
+        assert (err <= (128 + more) * U * mag[k] + h * np.abs(ref[k]) + TINY[stream]).all(), k
+    for d, dp in grads[1:]:
+        assert d is None or torch.equal(d, grads[0][0])
+        assert dp is None or torch.equal(dp, grads[0][1])
+    with pytest.raises(fm.FluxMIError):      # d_w_post is a sum over block / rms(block)
+        fm.fm_norm_residual_bwd(None, None, **kw, block=v["block"], d_w_post=torch.empty(N, device="cuda:0"))

@@ -312,8 +312,9 @@ extern "C" fm_status_t fm_norm_residual_bwd(
     a.d_y = d_y;
     a.d_out = d_out;
     a.out = out;
+    // without them block, w_post and rstd_post have no part in what is wanted
     a.block = need_b ? block : nullptr;
-    a.w_post = w_post;
+    a.w_post = need_b ? w_post : nullptr;
     a.w_pre = w_pre;
     a.gate = gate;
     a.rstd_post = rstd_post;
