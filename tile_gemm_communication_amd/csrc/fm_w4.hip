@@ -19,6 +19,7 @@
 // 2816 14.1 us (3.0 TB/s), over all 64 80 us (4.1 TB/s).
 #include <algorithm>
 
+#include "fm_w4_index.hpp"
 #include "fm_wave.hpp"
 
 namespace fm {
@@ -499,12 +500,12 @@ __device__ __forceinline__ void few_rows(const W4Args& a, const W4Work& b, char*
     W4Scales<E, GB, Z> sc[PF];
     // Where the wave's next step lies in the resources (bytes, scalar); past the last
     // step, that one again.
-    const int at0 = busy ? tile * 16 : 0;   // the wave's first column of the block's
+    const int n_tile = tile_column(n0, tile * 16, a.N), at0 = n_tile - n0;
     const int w_last = (at0 * a.blocks + max(s0 + steps - 1, 0)) * 64;
-    const int s_last = ((a.groups - 1) * a.N + n0 + at0) * 2 * a.some;
+    const int s_last = scale_offset(a.groups, a.groups, n_tile, a.N, a.some);
     const int s_step = a.N * (2 * GP);
     int lw = min((at0 * a.blocks + s0) * 64, w_last);
-    int ls = min((s0 * GP * a.N + n0 + at0) * 2 * a.some, s_last);
+    int ls = scale_offset(s0 * GP, a.groups, n_tile, a.N, a.some);
     auto load = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
       wr = load_codes(src, wo, lw);
       load_scales<E, GB, Z>(sr, src, sc16, ls, a.N * 2, s_last);
@@ -623,8 +624,9 @@ __device__ __forceinline__ void many_rows(const W4Args& a, const W4Work& b, char
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         w[nt] = load_codes(src, wo[nt], s * 64);
-        load_scales<E, GB, Z>(sc[nt], src, i16, (s * GP * a.N + n0 + nt * 16) * 2 * a.some, a.N * 2,
-                              ((a.groups - 1) * a.N + n0 + nt * 16) * 2 * a.some);
+        const int column = tile_column(n0, nt * 16, a.N);
+        load_scales<E, GB, Z>(sc[nt], src, i16, scale_offset(s * GP, a.groups, column, a.N, a.some),
+                              a.N * 2, scale_offset(a.groups, a.groups, column, a.N, a.some));
       }
     };
     f32x4 acc[MT][NT];
@@ -827,8 +829,8 @@ __global__ __launch_bounds__(kW4Threads) void w4_scatter_tiny(const W4TinyArgs a
   W4Source src =
       source_of<Z>(a, units ? __builtin_amdgcn_readlane(ex, pair_of(0)) : 0, n0, 16);
   const uint32_t wo = (uint32_t)c16 * a.blocks * 64 + q * 16;
-  const int last = ((a.groups - 1) * a.N + n0) * 2 * a.some;
-  const int first_s = min((s0 * GP * a.N + n0) * 2 * a.some, last);
+  const int last = scale_offset(a.groups, a.groups, n0, a.N, a.some);
+  const int first_s = scale_offset(s0 * GP, a.groups, n0, a.N, a.some);
   const int w_last = max(s0 + steps - 1, 0) * 64;
   int lw = min(s0 * 64, w_last), ls = first_s, li = 0;
   auto load = [&](u32x4& wr, W4Scales<E, GB, Z>& sr) {
