@@ -298,3 +298,21 @@ def test_binding_refuses_tensors_it_cannot_pass():
         fm.fm_norm_residual_bwd(x, None)
     with pytest.raises(ValueError):
         fm.fm_w4_pack(x, x)
+
+
+NONE = dict(block=None, resid=None, out=None, y=None, rq=None, rp=None)
+
+
+@pytest.mark.parametrize("kw", [dict(M=0), dict(M=0, gate=None, G=0), dict(M=0, wq=None, gate=None, G=0),
+                                dict(M=0, wp=None), dict(M=0, G=1)])
+def test_norm_of_no_rows(kw):
+    """Tensors without rows have no address; weights have."""
+    assert norm_call(**NONE, **kw) == OK
+    grads = dict(dy=None, do=None, out=None, block=None, rq=None, rp=None, dr=None, db=None,
+                 dwq=None, dwp=None, dg=None, ws=None, n=0)
+    assert norm_bwd_call(**grads, **kw) == OK
+
+
+def test_norm_of_no_rows_still_checks_the_rest():
+    assert norm_call(**NONE, M=0, dt=2, sd=2) == UNS and norm_call(**NONE, M=0, N=60) == INV
+    assert norm_call(**NONE, M=0, eps=-1.0) == INV

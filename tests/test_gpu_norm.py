@@ -235,3 +235,16 @@ def test_norm_backward_of_a_frozen_block(M, N, stream, block, G):
         assert dp is None or torch.equal(dp, grads[0][1])
     with pytest.raises(fm.FluxMIError):      # d_w_post is a sum over block / rms(block)
         fm.fm_norm_residual_bwd(None, None, **kw, block=v["block"], d_w_post=torch.empty(N, device="cuda:0"))
+
+
+@pytest.mark.parametrize("G", [0, 1, "rows"])
+def test_norm_without_rows(G):
+    """A batch of no tokens goes through forward and backward."""
+    import torch
+    e, r = torch.empty(0, 64, device="cuda:0", dtype=torch.bfloat16), torch.empty(0, device="cuda:0")
+    w = torch.ones(64, device="cuda:0", dtype=torch.bfloat16)
+    gate = {0: None, 1: w.view(1, 64), "rows": e}[G]
+    fm.fm_norm_residual(e, e, block=e, resid=e, w_post=w, w_pre=w, gate=gate, rstd_post=r, rstd_pre=r)
+    fm.fm_norm_residual_bwd(e, e, out=e, block=e, d_y=e, d_out=e, w_post=w, w_pre=w, gate=gate,
+                            rstd_post=r, rstd_pre=r)
+    torch.cuda.synchronize()

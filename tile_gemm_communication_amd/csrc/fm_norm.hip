@@ -138,10 +138,11 @@ extern "C" fm_status_t fm_norm_residual(fm_dtype_t dt, fm_dtype_t stream_dt, fm_
                                         hipStream_t stream) {
   const fm_status_t st = check_norm(dt, stream_dt, block_dt, M, N, gate, n_gates);
   if (st != FM_OK) return st;
-  if (!(eps >= 0.f) || (w_pre == nullptr) != (y == nullptr)) return FM_ERR_INVALID_ARG;
+  if (!(eps >= 0.f)) return FM_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return FM_OK;   // an empty batch's tensors have no addresses
+  if ((w_pre == nullptr) != (y == nullptr)) return FM_ERR_INVALID_ARG;
   if ((!block && (w_post || gate)) || (rstd_post && !w_post) || (rstd_pre && !w_pre))
     return FM_ERR_INVALID_ARG;
-  if (M == 0 || N == 0) return FM_OK;
   if ((!block && !resid) || (!out && !y)) return FM_ERR_INVALID_ARG;
   for (const void* p : {block, resid, w_post, w_pre, gate, (const void*)out, (const void*)y})
     if (!aligned16(p)) return FM_ERR_INVALID_ARG;

@@ -291,7 +291,8 @@ extern "C" fm_status_t fm_norm_residual_bwd(
   const fm_status_t st = check_norm(dt, stream_dt, block_dt, M, N, gate, n_gates);
   if (st != FM_OK) return st;
   if ((d_w_post && !w_post) || (d_w_pre && !w_pre) || (d_gate && !gate)) return FM_ERR_INVALID_ARG;
-  if (!d_resid && !d_block && !d_w_post && !d_w_pre && !d_gate) return FM_ERR_INVALID_ARG;
+  if (M > 0 && N > 0 && !d_resid && !d_block && !d_w_post && !d_w_pre && !d_gate)
+    return FM_ERR_INVALID_ARG;   // (an empty batch's tensors have no addresses)
   for (const void* p : {d_y, d_out, out, block, w_post, w_pre, gate, (const void*)d_resid,
                         (const void*)d_block, (const void*)d_w_post, (const void*)d_w_pre,
                         (const void*)d_gate, (const void*)ws})
