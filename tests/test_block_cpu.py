@@ -316,3 +316,27 @@ def test_norm_of_no_rows(kw):
 def test_norm_of_no_rows_still_checks_the_rest():
     assert norm_call(**NONE, M=0, dt=2, sd=2) == UNS and norm_call(**NONE, M=0, N=60) == INV
     assert norm_call(**NONE, M=0, eps=-1.0) == INV
+
+
+def test_binding_refuses_scalars_past_32_bits():
+    """The C interface takes 32 bits: a larger number is refused, not cut to its low half."""
+    import torch
+    m = _native()
+    x, i = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    p, off, big = torch.zeros(2, 8, 64, dtype=torch.uint8), torch.zeros(3, dtype=torch.int32), 1 << 32
+    s, sp = torch.zeros(2, 1, 8), torch.zeros(8, dtype=torch.int32)
+    h = torch.zeros(8, 8)
+    calls = [("score", m.moe_gate, (x, i, x, big, 0, 1.0, None, None, None, None, None, None)),
+             ("renormalize", m.moe_gate, (x, i, x, 0, -big, 1.0, None, None, None, None, None, None)),
+             ("score", m.moe_gate_bwd, (x, i, x, big + 1, 0, 1.0, None, None, None, None)),
+             ("expert_begin", m.moe_gather_gemm_w4, (x, i, p, s, h, sp, off, big, 32, None, None, 0)),
+             ("act", m.moe_gather_gemm_w4, (x, i, p, s, h, sp, off, 0, 32, None, None, big)),
+             ("expert_begin", m.moe_gemm_scatter_w4, (h, p, s, i, sp, off, x[:, :2], x, -big, 32, None, None,
+                                                      None))]
+    for name, f, args in calls:
+        with pytest.raises(ValueError, match=name + " does not fit"):
+            f(0, 0, *args)
+    with pytest.raises(TypeError):
+        m.moe_gate(0, 0, x, i, x, "0", 0, 1.0, None, None, None, None, None, None)
+    with pytest.raises(OverflowError):
+        m.moe_gate(0, 0, x, i, x, 1 << 64, 0, 1.0, None, None, None, None, None, None)

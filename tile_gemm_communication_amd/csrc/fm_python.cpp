@@ -89,6 +89,16 @@ struct Call {
     return FM_F32;
   }
 
+  // A scalar that the C interface takes in 32 bits.
+  int32_t i32(const char* name, PyObject* o) {
+    if (bad) return 0;
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) bad = true;
+    else if (v != (int32_t)v)
+      refuse(PyExc_ValueError, std::string(name) + " does not fit in 32 bits");
+    return (int32_t)v;
+  }
+
   // Sizes of a two-dimensional tensor that has to be there.
   const at::Tensor* matrix(const char* name, PyObject* o) {
     const at::Tensor* t = tensor(name, o);
@@ -133,18 +143,18 @@ PyObject* moe_gate(PyObject*, PyObject* const* v, Py_ssize_t n) {
   const int64_t T = x->size(0), E = x->size(1), topk = id->size(1);
   const at::ScalarType dt = x->scalar_type();
   const fm_dtype_t code = c.code(dt);
+  const int32_t score = c.i32("score", v[5]), renorm = c.i32("renormalize", v[6]);
   size_t bytes;
   void* ws = c.workspace(v[13], bytes);
   void *px = c.at("logits", v[2], dt, {T, E}), *pid = c.at("topk_ids", v[3], kInt, {T, topk}),
        *pw = c.at("topk_weights", v[4], kFloat, {T, topk}), *pb = c.at("bias", v[8], kFloat, {E}),
        *pm = c.mask(v[9], T), *pc = c.at("counts", v[10], kInt, {E + 1}),
        *ps = c.at("prob_sums", v[11], kFloat, {E}), *pl = c.at("loss", v[12], kFloat, {1});
-  const int64_t score = a.i(5), renorm = a.i(6);
   const float scale = a.f(7);
   const hipStream_t stream = a.stream(1);
   if (c.bad || PyErr_Occurred()) return nullptr;
   return done(c, fm_moe_gate(code, T, (int32_t)E, (int32_t)topk, (fm_gate_score_t)score,
-                             (int32_t)renorm, scale, px, (const float*)pb, (const uint8_t*)pm,
+                             renorm, scale, px, (const float*)pb, (const uint8_t*)pm,
                              (int32_t*)pid, (float*)pw, (int32_t*)pc, (float*)ps, (float*)pl, ws,
                              bytes, stream));
 }
@@ -160,16 +170,16 @@ PyObject* moe_gate_bwd(PyObject*, PyObject* const* v, Py_ssize_t n) {
   const int64_t T = x->size(0), E = x->size(1), topk = id->size(1);
   const at::ScalarType dt = x->scalar_type();
   const fm_dtype_t code = c.code(dt);
+  const int32_t score = c.i32("score", v[5]), renorm = c.i32("renormalize", v[6]);
   void *px = c.at("logits", v[2], dt, {T, E}), *pid = c.at("topk_ids", v[3], kInt, {T, topk}),
        *pd = c.at("d_logits", v[4], dt, {T, E}), *pm = c.mask(v[8], T),
        *pw = c.at("d_weights", v[9], kFloat, {T, topk}), *pc = c.at("counts", v[10], kInt, {E + 1}),
        *pl = c.at("d_loss", v[11], kFloat, {1});
-  const int64_t score = a.i(5), renorm = a.i(6);
   const float scale = a.f(7);
   const hipStream_t stream = a.stream(1);
   if (c.bad || PyErr_Occurred()) return nullptr;
   return done(c, fm_moe_gate_bwd(code, T, (int32_t)E, (int32_t)topk, (fm_gate_score_t)score,
-                                 (int32_t)renorm, scale, px, (const uint8_t*)pm,
+                                 renorm, scale, px, (const uint8_t*)pm,
                                  (const int32_t*)pid, (const float*)pw, (const int32_t*)pc,
                                  (const float*)pl, pd, stream));
 }
@@ -302,6 +312,7 @@ PyObject* moe_gather_gemm_w4(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (c.bad) return nullptr;
   const int64_t T = x->size(0), K = x->size(1), N = h->size(1), topk = id->size(1),
                 nl = p->size(0), group = a.i(10), G = groups_of(c, K, group);
+  const int32_t e0 = c.i32("expert_begin", v[9]), act = c.i32("act", v[13]);
   int64_t sp = 0;
   check_pairs(c, h, v[7], T * topk, sp);
   const at::ScalarType dt = x->scalar_type();
@@ -314,10 +325,9 @@ PyObject* moe_gather_gemm_w4(PyObject*, PyObject* const* v, Py_ssize_t n) {
        *po = c.at("sorted_pairs", v[7], kInt, {sp}),
        *pf = c.at("expert_offsets", v[8], kInt, {nl + 1}),
        *pz = c.at("zeros", v[12], kByte, {nl, G, N});
-  const int64_t e0 = a.i(9), act = a.i(13);
   const hipStream_t stream = a.stream(1);
   if (c.bad || PyErr_Occurred()) return nullptr;
-  return done(c, fm_moe_gather_gemm_w4(code, T, K, N, (int32_t)topk, (int32_t)e0, (int32_t)nl,
+  return done(c, fm_moe_gather_gemm_w4(code, T, K, N, (int32_t)topk, e0, (int32_t)nl,
                                        (int32_t)group, px, (const int32_t*)pid, pp, ps,
                                        (const uint8_t*)pz, ph, (int32_t*)po, (int32_t*)pf,
                                        (fm_act_t)act, ws, bytes, stream));
@@ -335,6 +345,7 @@ PyObject* moe_gemm_scatter_w4(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (c.bad) return nullptr;
   const int64_t T = w->size(0), topk = w->size(1), K = h->size(1), N = o->size(1),
                 nl = p->size(0), group = a.i(11), G = groups_of(c, K, group);
+  const int32_t e0 = c.i32("expert_begin", v[10]);
   int64_t sp = 0;
   check_pairs(c, h, v[6], T * topk, sp);
   const at::ScalarType dt = h->scalar_type();
@@ -350,10 +361,9 @@ PyObject* moe_gemm_scatter_w4(PyObject*, PyObject* const* v, Py_ssize_t n) {
        *pw = c.at("topk_weights", v[8], kFloat, {T, topk}),
        *po = c.at("out", v[9], kFloat, {T, N}), *pz = c.at("zeros", v[13], kByte, {nl, G, N}),
        *pa = c.at("add", v[14], kFloat, {T, N});
-  const int64_t e0 = a.i(10);
   const hipStream_t stream = a.stream(1);
   if (c.bad || PyErr_Occurred()) return nullptr;
-  return done(c, fm_moe_gemm_scatter_w4(code, T, N, K, (int32_t)topk, (int32_t)e0, (int32_t)nl,
+  return done(c, fm_moe_gemm_scatter_w4(code, T, N, K, (int32_t)topk, e0, (int32_t)nl,
                                         (int32_t)group, ph, pp, ps, (const uint8_t*)pz,
                                         (const int32_t*)pid, (const int32_t*)pq,
                                         (const int32_t*)pf, (const float*)pw, (const float*)pa,
