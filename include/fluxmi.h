@@ -527,9 +527,13 @@ fm_status_t fm_moe_gemm_scatter_noalloc(fm_dtype_t dt, int64_t T, int64_t hidden
  *   dt, logits  FM_F16, FM_BF16 or FM_F32, [T, n_experts]; n_experts 1..1024.
  *               An expert with logit -inf is closed: it is never chosen, and
  *               its share is 0.  A slot that finds no open expert gets id -1
- *               and weight 0, which every MoE call here passes over.  A NaN
- *               is never chosen; it (or +inf under a softmax) makes its row's
- *               shares, and so prob_sums and the loss, NaN.
+ *               and weight 0, which every MoE call here passes over.  A key
+ *               that is NaN or -inf is never chosen.  A NaN among a row's
+ *               logits (or +inf under a softmax) makes its shares NaN, and so
+ *               prob_sums, the loss and its row of d_logits.  Without a bias,
+ *               or with sigmoid scores, the row's other experts are chosen as
+ *               ever; with a bias under a softmax every key of the row is made
+ *               of those shares, and no slot finds an expert.
  *   topk        1..16 and <= n_experts.
  *   bias        fp32 [n_experts] or NULL; it only moves the choice.
  *   token_mask  uint8 [T] or NULL: tokens with 0 are padding.  Their logits are

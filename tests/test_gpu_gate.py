@@ -205,3 +205,45 @@ def test_gate_feeds_the_route(oracle):
     assert np.array_equal(off.cpu().numpy(), roff)
     assert np.array_equal(sp[:roff[-1]].cpu().numpy(), rsp)
     assert np.array_equal(np.diff(roff), c.cpu().numpy()[4:12])
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_gate_bias_and_rows_that_are_not_finite(dt, bad):
+    """Keys of a biased choice are made of scores: under a softmax one NaN (or +inf) makes all of
+    its row's NaN and the row finds no expert; sigmoid scores stand each for itself."""
+    import torch
+    rng = np.random.default_rng(21)
+    T, E, topk = 40, 24, 4
+    t = torch.from_numpy(rng.standard_normal((T, E))).to("cuda:0").to(_dtype(dt))
+    b = torch.from_numpy((0.1 * rng.standard_normal(E)).astype(np.float32)).to("cuda:0")
+    clean, b64 = t.double().cpu().numpy(), b.double().cpu().numpy()
+    t[7, 3] = bad
+    t[33] = bad
+    rest = [i for i in range(T) if i not in (7, 33)]
+    ids, w, c, s, loss = _forward(t, topk, score=0, bias=b)
+    want = ob.gate(clean, topk, 0, False, 1.0, b64)[0]
+    got = ids.cpu().numpy()
+    assert np.array_equal(got[rest], want[rest]) and (got[[7, 33]] == -1).all()
+    assert (w[[7, 33]] == 0).all() and torch.isfinite(w).all()
+    assert c[:E].sum().item() == topk * len(rest) and c[E].item() == T
+    assert torch.isnan(s).all() and torch.isnan(loss).all()
+    ids, w, c, s, loss = _forward(t, topk, score=1, bias=b)
+    want = clean.copy()
+    want[7, 3], want[33] = (-np.inf, -np.inf) if np.isnan(bad) else (bad, bad)   # chosen as +inf, never as NaN
+    want = ob.gate(want, topk, 1, False, 1.0, b64)[0]
+    assert np.array_equal(ids.cpu().numpy(), want) and torch.isfinite(w).all()
+
+
+def test_gate_bias_that_closes_experts():
+    """A bias of -inf or NaN keeps an expert from being chosen and leaves its share."""
+    import torch
+    x, x64 = _logits(50, 12, "fp32", 4)
+    b = np.zeros(12, np.float32)
+    b[[2, 5]] = -np.inf
+    want = ob.gate(x64, 3, 0, False, 1.0, b.astype(np.float64))
+    b[5] = np.nan
+    ids, w, c, s, loss = _forward(x, 3, bias=torch.from_numpy(b).to("cuda:0"))
+    assert np.array_equal(ids.cpu().numpy(), want[0]) and np.array_equal(c.cpu().numpy(), want[2])
+    np.testing.assert_allclose(w.cpu().numpy(), want[1], rtol=(6 * _range(x64) + 48) * U)
+    np.testing.assert_allclose(s.cpu().numpy(), want[3], rtol=(6 * _range(x64) + 304) * U)
