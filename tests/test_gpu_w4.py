@@ -6,8 +6,8 @@ truncates) and 4 instructions, 72 u of sum |x| (base + 15).  scale, zero and the
 fused multiply-adds add 4 u of the same; groups and waves are added up in chains of
 K / (32 * 8) and 8: (K / 256 + 8) u.  (Where the waves share several tiles the chains
 are up to K / 32 long, of terms within 15 sum |x| scale: up to K = 2185 that is within
-(K / 256 + 8) u of the magnitude below.)  With base 16 (bf16) or 64 (fp16) and
-|code - zero| <= 15 this is, for each output,
+(K / 256 + 8) u of the magnitude below.)  With a base of at most 16 (bf16) or 64
+(fp16; the kernels use 16 for both) and |code - zero| <= 15 this is, for each output,
   (K / 256 + 84) u * 2 (base + 15) * sum_k |x_k| scale_k.
 Two roundings follow for a weight and the sum over k (topk u), each 16-bit output rounds
 by eps / 2, activations have slopes up to 1.13 and add 16 u."""
@@ -354,3 +354,59 @@ def test_tensors_the_kernels_cannot_take_are_refused():
         fm.fm_gemm_w4(x, p, s, c.half(), 32)
     with pytest.raises(fm.FluxMIError):      # a row that starts between 16-byte boundaries
         fm.fm_gemm_w4(x.view(-1)[4:260].view(1, 256), p, s, c[:1], 32)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("M", [1, 3, 20, 50])
+def test_one_sided_integers_are_exact(M, dt):
+    """Large positive integers, as far from a sum that cancels as an activation's output gets.  A
+    group's sum of x (16 + code) is at most 128 * 2047 * 31 < 2^24, and so are its sum of x times
+    (16 + zero) and what the groups add up to (asserted): every number on the way is an integer
+    below 2^24, and the result exact, in whatever order it is summed."""
+    import torch
+    say(f"w4 one-sided M={M} {dt}")
+    K, N, group = 1024, 40, 128
+    rng = np.random.default_rng(M)
+    top = {"bf16": 256, "fp16": 2048}[dt]
+    x = rng.integers(top - top // 8, top, (M, K)).astype(np.float64)
+    codes = rng.integers(0, 16, (K, N)).astype(np.uint8)
+    zeros = rng.integers(5, 11, (K // group, N)).astype(np.uint8)
+    W = ob.w4_matrix(codes, np.ones((K // group, N)), zeros, group)
+    parts = np.einsum("mgk,gkn->gmn", x.reshape(M, -1, group), W.reshape(-1, group, N))
+    assert np.abs(parts).sum(axis=0).max() < 2 ** 24
+    one = torch.ones(K // group, N, device="cuda:0").to(_dtype(dt))
+    c = torch.empty(M, N, device="cuda:0")
+    fm.fm_gemm_w4(_dev(x, dt), _pack(codes), one, c, group, zeros=_dev(zeros))
+    assert not (_host(c) != x @ W).any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [1, 12, 60])
+def test_one_sided_integers_through_an_expert_are_exact(oracle, T, dt):
+    """The same through the experts' forms: scaled to 16-bit outputs by nothing (the combine's out is
+    fp32), with weights of 1 or 0.5 and sums that stay integers or halves below 2^23."""
+    say(f"w4 one-sided experts T={T} {dt}")
+    E, K, N, topk, group = 4, 512, 40, 2, 128
+    rng = np.random.default_rng(T)
+    top = {"bf16": 256, "fp16": 2048}[dt]
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :topk].astype(np.int32)
+    roff, rsp = oracle.moe_route(ids, 0, E)
+    h = rng.integers(top - top // 8, top, (T * topk, K)).astype(np.float64)
+    codes = rng.integers(0, 16, (E, K, N)).astype(np.uint8)
+    zeros = rng.integers(6, 10, (E, K // group, N)).astype(np.uint8)
+    w = rng.choice([0.5, 1.0], (T, topk)).astype(np.float32)
+    ref, total = np.zeros((T, N)), np.zeros((T, N))
+    for e in range(E):
+        p = rsp[roff[e]:roff[e + 1]]
+        W = ob.w4_matrix(codes[e], np.ones((K // group, N)), zeros[e], group)
+        hr = h[roff[e]:roff[e + 1]]
+        np.add.at(ref, p // topk, w.reshape(-1)[p][:, None] * (hr @ W))
+        parts = np.einsum("mgk,gkn->gmn", hr.reshape(len(p), K // group, group), W.reshape(-1, group, N))
+        np.add.at(total, p // topk, np.abs(parts).sum(axis=0))
+    assert total.max() < 2 ** 23
+    import torch
+    out = torch.empty(T, N, device="cuda:0")
+    fm.fm_moe_gemm_scatter_w4(_dev(h, dt), _pack(codes), torch.ones(E, K // group, N, device="cuda:0").to(_dtype(dt)),
+                              _dev(ids), _dev(rsp.astype(np.int32)), _dev(roff.astype(np.int32)), _dev(w), out, 0,
+                              group, fm.moe_w4_workspace(T, topk, N), zeros=_dev(zeros))
+    assert not (_host(out) != ref).any()

@@ -7,11 +7,14 @@
 //   few_rows  up to 4 rows (experts): x in LDS, 4x4x4 products, a tile a wave
 //   many_rows 16, 32 or 48 rows at a time: 16x16x32 products, K over the waves
 // A code c enters the matrix core exactly, without a conversion, as the 16-bit
-// number base + c, whose bit pattern is the code shifted into a constant's
-// mantissa (bf16: base 16, fp16: base 64).  With t = sum x (base + c) and
-// S = sum x over one group of K (a matrix product with ones),
-//   sum x (c - zero) scale = scale * (t - (base + zero) * S),
-// so that scale and zero cost two fused multiply-adds a group and output.
+// number 16 + c, whose bit pattern is the code shifted to the top of a constant's
+// mantissa.  With t = sum x (16 + c) and S = sum x over one group of K (a matrix
+// product with ones),
+//   sum x (c - zero) scale = scale * (t - (16 + zero) * S),
+// so that scale and zero cost two fused multiply-adds a group and output.  16 is the
+// smallest base whose sums have one exponent: what t loses to rounding grows with it
+// (fp16 has bits for a base of 64 at one shift less in eight codes; with x of one
+// sign that lost two more bits of the result).
 //
 // Measured (kernel alone; the bytes of codes, scales and zeros over that time):
 // 1 x 6144 x 12288 fp16 9.4 us (4.1 TB/s), 45 x 12288 x 6144 bf16 25 us (1.9 TB/s:
@@ -67,8 +70,8 @@ struct W4Consts {
   u32x4 ones;
   __device__ __forceinline__ W4Consts() {
     constexpr bool half = E::id == FM_F16;
-    mask = half ? 0x00F000F0u : 0x00780078u;
-    base = half ? 0x54005400u : 0x41804180u;   // 64, ulp 1/16, or 16, ulp 1/8
+    mask = half ? 0x03C003C0u : 0x00780078u;
+    base = half ? 0x4C004C00u : 0x41804180u;   // 16; the mask is where 1 + 2 + 4 + 8 lie
     const uint32_t one = half ? 0x3C003C00u : 0x3F803F80u;
     ones = u32x4{one, one, one, one};
     asm volatile("" : "+s"(mask));
@@ -77,17 +80,16 @@ struct W4Consts {
   }
 };
 
-// Eight codes of a word as base + code, pair i holding nibbles i and i + 4.
+// Eight codes of a word as 16 + code, pair i holding nibbles i and i + 4.
 __device__ __forceinline__ u32x4 codes8(const W4Consts<BF16>& k, uint32_t w) {
   return {((w << 3) & k.mask) | k.base, ((w >> 1) & k.mask) | k.base,
           ((w >> 5) & k.mask) | k.base, ((w >> 9) & k.mask) | k.base};
 }
 __device__ __forceinline__ u32x4 codes8(const W4Consts<F16>& k, uint32_t w) {
-  return {((w << 4) & k.mask) | k.base, (w & k.mask) | k.base, ((w >> 4) & k.mask) | k.base,
-          ((w >> 8) & k.mask) | k.base};
+  return {((w << 6) & k.mask) | k.base, ((w << 2) & k.mask) | k.base,
+          ((w >> 2) & k.mask) | k.base, ((w >> 6) & k.mask) | k.base};
 }
-__device__ constexpr float code_base(BF16) { return 16.f; }
-__device__ constexpr float code_base(F16) { return 64.f; }
+constexpr float kCodeBase = 16.f;
 
 enum W4Mode { kDense16, kDense32, kGather, kScatter };
 
@@ -186,9 +188,9 @@ struct W4Scales {
   __device__ __forceinline__ float scale(int g) const {
     return (float)__builtin_bit_cast(typename Elem<E>::type, (uint16_t)s[g]);
   }
-  // -(base + zero)
+  // -(16 + zero)
   __device__ __forceinline__ float offset(int g) const {
-    return Z ? -code_base(E()) - (float)z[Z ? g : 0] : -code_base(E()) - 8.f;
+    return Z ? -kCodeBase - (float)z[Z ? g : 0] : -kCodeBase - 8.f;
   }
 };
 
