@@ -16,11 +16,13 @@ def pytest_configure(config):
 @pytest.fixture(scope="session")
 def built_library():
     """libfluxmi.so, compiled first (hipcc, gfx950; no GPU needed) when a fresh
-    checkout has none yet."""
+    checkout has none yet, with the binding's module beside it."""
     import tile_gemm_communication_amd as fm
     from tile_gemm_communication_amd import build
     if not os.path.exists(fm.LIB_PATH) or not os.path.exists(build.RESOURCES):
         build.build(verbose=False)
+    elif not os.path.exists(build.MODULE):
+        build.build_module()
     return fm.lib()
 
 

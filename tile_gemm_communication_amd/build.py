@@ -1,8 +1,9 @@
 """Build libfluxmi.so (HIP, gfx950 only) and the binding's module in-tree.
 
 Every source under csrc/ is compiled by hipcc for gfx950 and linked into one
-shared library next to this file, which the Python binding loads; _fluxmi.so
-(host code against torch's headers) checks tensors for it.  Packed
+shared library next to this file, which the Python binding loads; it needs
+hipcc alone.  _fluxmi.so (host code against torch's headers) checks tensors for
+the binding and is built where torch is installed.  Packed
 fp32 VALU ops are disabled for every device compile.  The compiler's
 per-kernel register and scratch figures are kept in
 _build/kernel_resources.json, which the CPU tests check.
@@ -11,6 +12,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import json
 import os
 import re
@@ -97,24 +99,36 @@ def _link_module(obj: str) -> None:
     os.replace(tmp, MODULE)
 
 
-def build(verbose: bool = True) -> str:
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sources()
-    jobs = min(len(srcs) + 1, int(os.environ.get("MAX_JOBS", "8")))
-    with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
-        module = ex.submit(_compile_module)
-        done = list(ex.map(_compile, srcs))
-        module = module.result()
-    objs = [o for o, _ in done]
+def build_library(ex: cf.Executor) -> None:
+    """libfluxmi.so and the compiler's resource figures."""
+    done = list(ex.map(_compile, sources()))
     with open(RESOURCES, "w") as f:
         json.dump([k for _, ks in done for k in ks], f, indent=0)
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
+    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *[o for o, _ in done], "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_module(module)
+
+
+def build_module() -> None:
+    """_fluxmi.so beside a library that is built."""
+    _link_module(_compile_module())
+
+
+def build(verbose: bool = True) -> str:
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    have_torch = importlib.util.find_spec("torch") is not None
+    jobs = min(len(sources()) + 1, int(os.environ.get("MAX_JOBS", "8")))
+    with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
+        module = ex.submit(_compile_module) if have_torch else None
+        build_library(ex)
+        if module:
+            _link_module(module.result())
+        else:
+            print("torch is not installed: _fluxmi.so, which the Python binding of the router, "
+                  "norms and 4-bit products needs, is not built", file=sys.stderr)
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB
