@@ -410,3 +410,58 @@ def test_one_sided_integers_through_an_expert_are_exact(oracle, T, dt):
                               _dev(ids), _dev(rsp.astype(np.int32)), _dev(roff.astype(np.int32)), _dev(w), out, 0,
                               group, fm.moe_w4_workspace(T, topk, N), zeros=_dev(zeros))
     assert not (_host(out) != ref).any()
+
+
+ONE_TOKEN = [  # T, hidden, ffn, E, nl, e0, topk, group, dt, zeros, act: at most three pairs
+    (1, 264, 72, 8, 8, 0, 1, 32, "bf16", True, 3),         # one pair
+    (1, 264, 72, 8, 8, 8, 1, 32, "bf16", True, 3),         # ... of another rank
+    (1, 4096, 2816, 4, 4, 0, 1, 128, "fp16", False, 2),
+    (1, 136, 16392, 2, 2, 0, 1, 64, "bf16", True, 0),      # two tiles a block, the last block's second past N
+    (1, 24576, 40, 3, 3, 0, 1, 32, "fp16", True, 1),
+    (1, 72, 2816, 8, 8, 0, 2, 128, "bf16", False, 3),      # three steps of a wave on each of two pairs
+    (1, 72, 2816, 8, 4, 0, 2, 64, "fp16", True, 0),
+    (1, 40, 1288, 4, 4, 0, 2, 32, "bf16", True, 2),        # a wave without steps, a short last block
+    (1, 40, 2816, 8, 8, 0, 3, 64, "fp16", True, 3),
+    (1, 56, 16384, 8, 8, 0, 3, 128, "bf16", False, 0),     # three rows nearly fill LDS
+    (1, 24, 12296, 8, 4, 2, 3, 32, "fp16", True, 1),
+    (3, 88, 1160, 4, 4, 0, 1, 32, "bf16", True, 0),
+    (3, 88, 2824, 8, 4, 4, 1, 64, "fp16", True, 2),
+    (2, 2056, 1416, 4, 4, 0, 1, 128, "bf16", False, 3),
+    (2, 8, 136, 3, 1, 1, 1, 32, "fp16", True, 0),
+]
+
+
+@pytest.mark.parametrize("T,hidden,ffn,E,nl,e0,topk,group,dt,zeros,act", ONE_TOKEN)
+def test_gather_w4_of_few_pairs(oracle, T, hidden, ffn, E, nl, e0, topk, group, dt, zeros, act):
+    test_gather_w4(oracle, T, hidden, ffn, E, nl, e0, topk, group, dt, zeros, act)
+
+
+@pytest.mark.parametrize("T,hidden,ffn,E,nl,e0,topk,group,dt,zeros,act", ONE_TOKEN)
+def test_scatter_w4_of_few_pairs(oracle, T, hidden, ffn, E, nl, e0, topk, group, dt, zeros, act):
+    test_scatter_w4(oracle, T, hidden, ffn, E, nl, e0, topk, group, dt, zeros, act)
+
+
+def test_scatter_w4_of_an_expert_named_twice(oracle):
+    """Both slots of one token name one expert: two rows, two weights."""
+    import torch
+    K, N, group = 1416, 40, 64
+    rng = np.random.default_rng(8)
+    codes, s, z = _weights((3,), K, N, group, "bf16", True, rng)
+    h, w = _dev(rng.standard_normal((2, K)), "bf16"), rng.random((1, 2)).astype(np.float32)
+    out = torch.empty(1, N, device="cuda:0")
+    fm.fm_moe_gemm_scatter_w4(h, _pack(codes), s, _dev(np.array([[5, 5]], np.int32)),
+                              _dev(np.array([0, 1], np.int32)), _dev(np.array([0, 2, 2, 2], np.int32)), _dev(w),
+                              out, 5, group, fm.moe_w4_workspace(1, 2, N), zeros=z)
+    v = _host(h) @ ob.w4_matrix(codes[0], _host(s)[0], z[0].cpu().numpy(), group)
+    lim = w.astype(np.float64) @ (_bound(_host(h), _host(s)[0], K, group, "bf16") + 4 * U * np.abs(v))
+    assert (np.abs(_host(out) - w.astype(np.float64) @ v) <= lim + 2 * U * np.abs(w @ v)).all()
+
+
+@pytest.mark.parametrize("N,K,group,dt,out,zeros", [
+    (16392, 520, 64, "bf16", "fp32", True),                # two tiles a block
+    (32776, 136, 32, "fp16", "fp16", True),                # four
+    (65544, 264, 128, "bf16", "bf16", False),              # eight
+    (65560, 1032, 32, "fp16", "fp32", False),
+])
+def test_gemm_w4_of_one_long_row(N, K, group, dt, out, zeros):
+    test_gemm_w4(1, N, K, group, dt, out, zeros)
