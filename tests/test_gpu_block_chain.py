@@ -191,3 +191,79 @@ def test_two_chains_at_once():
     torch.cuda.synchronize()
     _same(ra, a.results())
     _same(rb, b.results())
+
+
+def _codes(packed, K):
+    """Codes [K, N] of packed bytes [N, row], one nibble at a time; packing them again gives the bytes."""
+    words = packed.reshape(packed.shape[0], -1, 64).copy().view("<u4")     # [N, block, 16]
+    out = np.zeros((words.shape[1] * 128, packed.shape[0]), np.uint8)
+    for w in range(16):
+        for p in range(8):
+            k = 32 * (w % 4) + 8 * (w // 4) + (2 * p if p < 4 else 2 * (p - 4) + 1)
+            out[k::128] = ((words[:, :, w] >> np.uint32(4 * p)) & 15).T
+    assert np.array_equal(ob.w4_pack(out), packed)
+    return out[:K]
+
+
+def _norm_matches(out, y, rq, rp, block, resid, w_post, w_pre, gate, scale):
+    """Stored stream, normed rows and both 1 / rms against the definition on the same inputs."""
+    ro, ry, rrq, rrp, mag = ob.norm(*(_host(t) for t in (block, resid, w_post, w_pre)),
+                                    None if gate is None else _host(gate), scale, EPS)
+    assert (np.abs(_host(out) - ro) <= 32 * U * mag + 2.0 ** -8 * np.abs(ro)).all()
+    np.testing.assert_allclose(_host(rq), rrq, rtol=24 * U)
+    # the rms of out moves by at most the largest relative error of its rows' terms
+    rel = 32 * U * np.linalg.norm(mag, axis=1) / np.linalg.norm(ro, axis=1)
+    assert (np.abs(_host(rp) / rrp - 1) <= 24 * U + rel).all()
+    lim = (32 * U * mag + (28 * U + rel)[:, None] * np.abs(ro)) * rrp[:, None] * np.abs(_host(w_pre))
+    assert (np.abs(_host(y) - ry) <= lim + 2.0 ** -8 * np.abs(ry)).all()
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_products_and_norms_of_the_chain(oracle, four):
+    """The steps between: both dense products, the route, both expert layers and both norms, each on
+    the bits that the step before left.  A product of 16-bit numbers is exact in fp32 and each of its K
+    additions is off by at most 2 u (if it truncates): 2 K u of sum |a| |b|.  The 4-bit ones, with base
+    16: (K / 256 + 84) u * 62 of sum |x| scale."""
+    import torch
+    say(f"chain products four={four}")
+    c = Chain(8, four)
+    c.run()
+    torch.cuda.synchronize()
+
+    def near(got, a, b):
+        return (np.abs(_host(got) - _host(a) @ _host(b)) <=
+                2 * a.shape[1] * U * (np.abs(_host(a)) @ np.abs(_host(b))) + 1e-38).all()
+
+    assert near(c.slices, c.a, c.w) and near(c.logits, c.y, c.w_r)
+    _norm_matches(c.out, c.y, c.rq, c.rp, c.slices, c.resid, c.w_post, c.w_pre, None, 1.0)
+    _norm_matches(c.out2, c.y2, c.rq2, c.rp2, c.moe, c.out, c.w_post, c.w_pre, c.gate, 0.5)
+    ids = c.ids.cpu().numpy()
+    roff, rsp = oracle.moe_route(ids, 0, E)
+    assert np.array_equal(c.off.cpu().numpy(), roff) and np.array_equal(c.sp.cpu().numpy(), rsp)
+    assert roff[-1] == T * TOPK
+
+    def layer(i, x, e):
+        """x [rows, K] times expert e's matrix of layer i, and the bound of its error."""
+        K = x.shape[1]
+        if not four:
+            W = _host((c.w1, c.w2)[i][e])
+            return x @ W, 2 * K * U * (np.abs(x) @ np.abs(W))
+        packed, scales = c.m[i]
+        s = _host(scales[e])
+        W = ob.w4_matrix(_codes(packed[e].cpu().numpy(), K), s, None, GROUP)
+        return x @ W, (K / 256 + 84) * U * 62 * (np.abs(x) @ s[np.arange(K) // GROUP])
+
+    y, h, wts = _host(c.y), _host(c.h), _host(c.wts).reshape(-1)
+    moe, lim_moe = np.zeros((T, HID)), np.zeros((T, HID))
+    for e in range(E):
+        rows = slice(roff[e], roff[e + 1])
+        p = rsp[rows]
+        if len(p) == 0:
+            continue
+        v, lim = layer(0, y[p // TOPK], e)
+        ref = v / (1 + np.exp(-v))                                # slope at most 1.13
+        assert (np.abs(h[rows] - ref) <= 1.13 * lim + 16 * U * np.abs(v) + 2.0 ** -8 * np.abs(ref) + 1e-38).all()
+        v, lim = layer(1, h[rows], e)
+        np.add.at(moe, p // TOPK, wts[p][:, None] * v)
+        np.add.at(lim_moe, p // TOPK, wts[p][:, None] * (lim + (TOPK + 2) * U * np.abs(v)))
+    assert (np.abs(_host(c.moe) - moe) <= lim_moe + 2 * U * np.abs(moe) + 1e-38).all()
