@@ -458,8 +458,7 @@ __device__ __forceinline__ void few_rows(const W4Args& a, const W4Work& b, char*
   const int steps = busy ? min(a.blocks, s0 + per) - s0 : 0;
   const W4Consts<E> consts;
 
-  for (int64_t m0 = MODE <= kDense32 ? (int64_t)blockIdx.z * R : 0; m0 < rows;
-       m0 += MODE <= kDense32 ? (int64_t)gridDim.z * R : R) {
+  for (int64_t m0 = 0; m0 < rows; m0 += R) {
     const int count = (int)min((int64_t)R, rows - m0);
     // x rows into LDS in pieces of 16 bytes a lane, zeros past K (the codes there
     // may be anything).  The first pieces are asked for ahead of the weights.
