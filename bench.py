@@ -46,27 +46,46 @@ PEAK_TFLOPS = 2516.6          # MI355X dense fp16/bf16 MFMA: 256 CU x 2.4 GHz x 
 # WRITE_SIZE runs of `bench.py --steps 2 --warmup 1 --no-ect --no-cpu-baseline
 # --serial-arrival` (KiB per dispatch, averaged), scaled by the factors a
 # known-size copy (`bench.py --copy-probe 256`) gives: FETCH_SIZE x2.0,
-# WRITE_SIZE x1.0.  Keyed by the digest of the kernel sources they were taken
-# on: after any change to csrc/ they no longer apply and traffic is null.
-TRAFFIC_DIGEST = "5770d0f34cc2c329"
+# WRITE_SIZE x1.0.  Keyed by the digest of the sources that these kernels are
+# compiled from: after any change to them the bytes no longer apply and traffic
+# is null.
+TRAFFIC_DIGEST = "1e77821e5611836b"
 TRAFFIC_BYTES = {             # op name -> (read bytes, written bytes) per call
-    "ag_gemm": (1119624959, 50328564),
-    "gemm_rs": (1115677704, 201317328),
-    "moe_gather_gemm": (1337121233, 172566322),
-    "moe_gemm_scatter": (2224136528, 501668013),
+    "ag_gemm": (1114557629, 50328557),
+    "gemm_rs": (1133003830, 201318938),
+    "moe_gather_gemm": (1338164601, 172589618),
+    "moe_gemm_scatter": (2246943084, 501667954),
 }
 
 
+def step_sources():
+    """The sources of the step's kernels: the dense, MoE and push files and every
+    file of csrc/ that they include."""
+    import re
+    csrc = os.path.join(ROOT, "tile_gemm_communication_amd", "csrc")
+    todo, seen = ["fm_gemm.hip", "fm_moe.hip", "fm_push.hip"], set()
+    while todo:
+        name = todo.pop()
+        path = os.path.join(csrc, name)
+        if name in seen or not os.path.exists(path):   # include/ holds no kernel code
+            continue
+        seen.add(name)
+        with open(path) as f:
+            todo += re.findall(r'^#include "([^"]+)"', f.read(), re.M)
+    return [os.path.join(csrc, name) for name in sorted(seen)]
+
+
 def source_digest() -> str:
-    """sha256 over the library's kernel sources (names and contents)."""
-    import glob
+    """sha256 over the step kernels' sources (names and contents)."""
     import hashlib
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "tile_gemm_communication_amd", "csrc", "*"))):
+    for f in step_sources():
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
+
+
 METRIC = "fused AG/RS-GEMM TFLOP/s & % MFMA peak; ECT vs non-split GEMM"
 
 

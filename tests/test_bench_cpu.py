@@ -93,3 +93,21 @@ def test_time_rounds_takes_turns_and_the_median(monkeypatch):
     med = b.time_rounds([("a", lambda: "a"), ("b", lambda: "b")], iters=1, rounds=3)
     assert calls == ["a", "b"] * 3
     assert med == {"a": 3.0, "b": 4.0}
+
+
+def test_traffic_is_keyed_by_the_step_kernels_alone():
+    """The counters' bytes hold while the sources that the step's kernels are compiled from are those
+    they were taken on; sources of other operators do not count."""
+    b = _bench()
+    names = [os.path.basename(f) for f in b.step_sources()]
+    assert {"fm_gemm.hip", "fm_moe.hip", "fm_push.hip", "fm_tile.hpp", "fm_sched.hpp", "fm_common.hpp"} == set(names)
+    assert names == sorted(names)
+    for op in ("ag_gemm", "gemm_rs", "moe_gather_gemm", "moe_gemm_scatter"):
+        t = b.traffic(op)
+        assert t["traffic"] == t["traffic_read"] + t["traffic_write"] > 0
+
+
+def test_traffic_of_other_sources_is_null(monkeypatch):
+    b = _bench()
+    monkeypatch.setattr(b, "TRAFFIC_DIGEST", "0" * 16)
+    assert b.traffic("ag_gemm") == {"traffic": None}
