@@ -664,8 +664,10 @@ fm_status_t fm_w4_pack(int64_t n_matrices, int64_t K, int64_t N, const uint8_t* 
  *   ab      FM_F16 or FM_BF16: A and scales;  c  ab or FM_F32.
  *   packed  as above, 16-byte aligned; scales 16-byte aligned.
  * Codes enter the matrix cores exactly; products are summed in fp32 group by
- * group and scaled there.  A must be finite: an infinite or NaN A[m, k] makes
- * row m of C NaN or infinite.
+ * group and scaled there: codes as 16 + code, with 16 + zero times the sum of A
+ * taken off afterwards, so a result's error is relative to sum |A| (16 + code)
+ * scale.  A must be finite, and 31 times the sum of a group's |A| below 2^128; an
+ * infinite or NaN A[m, k] makes row m of C NaN or infinite.
  */
 fm_status_t fm_gemm_w4(fm_dtype_t ab, fm_dtype_t c, int64_t M, int64_t N, int64_t K,
                        int32_t group, const void* A, const void* packed, const void* scales,

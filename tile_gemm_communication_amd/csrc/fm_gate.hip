@@ -7,9 +7,11 @@
 // are fp32; the keys of a biased choice are fp64, because a rounded score next
 // to another one would change which experts are taken.
 //
-// Measured: 16384 x 64 bf16, top 2, with statistics 4.9 us (bound by the steps of
-// the choice, not by the 2.4 MB) and 4.9 for the join; one token 2.3.  Backward of
-// 65521 x 256 fp32, top 8, 39 us: 3.5 TB/s, bound by the exchanges a row.
+// Measured: 16384 x 64 bf16, top 2, with statistics 4.9 us (the steps of the choice one
+// after another, not the 2.4 MB: two waves a SIMD, which wait 60% of their time) and 4.9
+// for the join; one token 2.3.  65536 x 256, top 8, 72 us: 62% of the cycles issue the
+// choice's vector instructions.  Backward of 65521 x 256 fp32, top 8, 39 us: 3.5 TB/s,
+// vector instructions in 64% of the cycles and LDS exchanges in 31%.
 #include <algorithm>
 
 #include "fm_wave.hpp"

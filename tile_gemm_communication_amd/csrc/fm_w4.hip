@@ -3,8 +3,9 @@
 //
 // With few rows the weights are all there is to read, so the kernels are built to
 // stream them in whole cache lines, two steps of 128 k ahead.  Three shapes:
-//   w4_one    one row: 4x4x4 products whose diagonal is what is wanted
-//   few_rows  up to 4 rows (experts): x in LDS, 4x4x4 products, a tile a wave
+//   w4_one    one row (few_rows): 4x4x4 products whose diagonal is what is wanted
+//   few_rows  one row so, or up to 4 (experts) with 16x16x32 products: x in LDS, the
+//             waves share the tiles of a block and K
 //   many_rows 16, 32 or 48 rows at a time: 16x16x32 products, K over the waves
 // A code c enters the matrix core exactly, without a conversion, as the 16-bit
 // number 16 + c, whose bit pattern is the code shifted to the top of a constant's
@@ -16,10 +17,14 @@
 // (fp16 has bits for a base of 64 at one shift less in eight codes; with x of one
 // sign that lost two more bits of the result).
 //
-// Measured (kernel alone; the bytes of codes, scales and zeros over that time):
-// 1 x 6144 x 12288 fp16 9.4 us (4.1 TB/s), 45 x 12288 x 6144 bf16 25 us (1.9 TB/s:
-// bound by x, which 128 blocks each read), 61 tokens over 8 of 64 experts of 4096 x
-// 2816 14.1 us (3.0 TB/s), over all 64 80 us (4.1 TB/s).
+// Measured (kernel alone, three matrices in turn, which the Infinity Cache holds where
+// one is below 80 MB; the bytes of codes, scales and zeros over that time): 1 x 6144 x
+// 12288 fp16 9.5 to 10 us (4 TB/s; a call with the weights from HBM 13.4), 61 tokens
+// over 8 of 64 experts of 4096 x 2816 14.1 us (3.0 TB/s), over all 64 80 to 83 us (4.0
+// TB/s): waves wait for memory half of their time or more.  45 x 12288 x 6144 bf16 25
+// to 26 us (1.9 TB/s): 256 blocks, whose LDS leaves room for one a compute unit, with
+// two waves a SIMD that issue vector instructions in 48% of the cycles (group 32: eight
+// fused multiply-adds a product), use LDS in 38% and the matrix core in 16%.
 #include <algorithm>
 
 #include "fm_w4_index.hpp"
@@ -38,7 +43,9 @@ constexpr int kW4MaxExperts = 64;
 constexpr int kFewRows = 4;
 // Mean rows of an expert up to which w4_mixed runs, with the route in its own blocks
 // for the first layer (8 experts, 4096 x 2816: 61 tokens 22.6 us, as two launches of
-// route and w4_many 31.5).
+// route and w4_many 31.5).  The mean is the host's bound, tokens x topk over the local
+// experts: on one rank of eight it is eight times too high, and 68 tokens on 8 of 64
+// experts already take the other form (32 us, 61 tokens 16).
 constexpr int64_t kMixedRows = 16;
 
 __device__ __forceinline__ f32x4 mfma16(F16, u32x4 a, u32x4 b, f32x4 c) {
@@ -742,7 +749,8 @@ __device__ __forceinline__ bool find_work(const W4Args& a, int columns, W4Work& 
   return b.rows > 0;
 }
 
-// One row (6144 x 12288: 12.7 us a call, few_rows with 4 rows 16.7, many_rows 14.3).
+// One row (6144 x 12288, weights from HBM: 12.7 us a call, few_rows with 4 rows 16.7,
+// many_rows 14.3).
 template <typename E, int GB, bool Z, W4Mode MODE, bool ROUTE>
 __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(4))) void w4_one(
     const W4Args a) {
