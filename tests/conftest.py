@@ -21,7 +21,7 @@ def built_library():
     from tile_gemm_communication_amd import build
     if not os.path.exists(fm.LIB_PATH) or not os.path.exists(build.RESOURCES):
         build.build(verbose=False)
-    elif not os.path.exists(build.MODULE):
+    elif not os.path.exists(build.MODULE) and build.have_torch():
         build.build_module()
     return fm.lib()
 

@@ -112,6 +112,10 @@ def build_library(ex: cf.Executor) -> None:
     os.replace(tmp, LIB)
 
 
+def have_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def build_module() -> None:
     """_fluxmi.so beside a library that is built."""
     _link_module(_compile_module())
@@ -119,10 +123,9 @@ def build_module() -> None:
 
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    have_torch = importlib.util.find_spec("torch") is not None
     jobs = min(len(sources()) + 1, int(os.environ.get("MAX_JOBS", "8")))
     with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
-        module = ex.submit(_compile_module) if have_torch else None
+        module = ex.submit(_compile_module) if have_torch() else None
         build_library(ex)
         if module:
             _link_module(module.result())
