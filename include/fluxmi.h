@@ -14,7 +14,10 @@
  * loss (fm_moe_gate, fm_moe_gate_bwd), the norms, gate and residual add between
  * two blocks (fm_norm_residual, fm_norm_residual_bwd), and the products of a
  * decode step with 4-bit weights (fm_gemm_w4, fm_moe_gather_gemm_w4,
- * fm_moe_gemm_scatter_w4),
+ * fm_moe_gemm_scatter_w4); in a dense block: dropout (fm_dropout), bias, dropout,
+ * residual add and layer norm between two products (fm_layer_norm,
+ * fm_layer_norm_bwd), and products in 8-bit integers (fm_quant_i8, fm_gemm_i8,
+ * fm_linear_i8),
  * plus the AllGather variants fm_ag_gemm_pull (chunks read in place),
  * fm_ag_gemm_producers (copies done by workgroups of the same launch),
  * fm_moe_ag_gather_gemm (MoE layer 0 behind a token AllGather) with its
@@ -710,6 +713,128 @@ fm_status_t fm_moe_gemm_scatter_w4(fm_dtype_t dt, int64_t T, int64_t hidden, int
                                    const int32_t* expert_offsets, const float* topk_weights,
                                    const float* add, float* out, void* ws, size_t ws_bytes,
                                    hipStream_t stream);
+
+/*
+ * fm_dropout -- y = x * s where an element is kept, 0 where it is dropped (whatever x
+ * is there), from a counter-based generator: the mask is a function of seed, offset
+ * and place alone and is never stored.  The backward pass is the same call on the
+ * gradient.  Element (i, j) has the 16-bit number
+ *   half c % 8 of philox4x32_10(counter, key),  r = row_begin + i, c = col_begin + j,
+ *   counter = (c / 8, r, low and high word of rng[1] + draw),  key = rng[0],
+ * halves counted from the low end of word 0, and is kept if that is below t;
+ *   t = (1 - p) * 65536 rounded,   s = 65536 / t.
+ * (Philox: Salmon, Moraes, Dror, Shaw, "Parallel Random Numbers: As Easy as 1, 2, 3",
+ * 2011.)  A GPU that holds some rows or columns of a tensor draws with row_begin and
+ * col_begin what one that holds all of it would.
+ *   dt         FM_F16, FM_BF16 or FM_F32.   x, y  [M, N]; y may be x itself.
+ *   p          share of dropped elements, 0..1; 0 copies, 1 clears.
+ *   rng        device uint64 [2]: seed and offset; read when the kernel runs, so a
+ *              captured graph draws anew if the program advances rng[1] between
+ *              replays.  NULL only with p = 0.
+ *   draw       added to the offset (both wrap round): one number for each place of a
+ *              program that draws, the same in forward and backward.
+ *   row_begin, col_begin  >= 0; col_begin a multiple of 8; row_begin + M at most
+ *              2^32, col_begin + N at most 2^34.
+ */
+fm_status_t fm_dropout(fm_dtype_t dt, int64_t M, int64_t N, const void* x, float p,
+                       const uint64_t* rng, int64_t draw, int64_t row_begin, int64_t col_begin,
+                       void* y, hipStream_t stream);
+
+/*
+ * fm_layer_norm -- what lies between two products of a dense block's residual stream,
+ * in one pass.  For each row
+ *   out = resid + dropout(block + bias)
+ *   y   = (out - mean) * rstd * w + b     mean, rstd = 1 / sqrt(variance + eps) of out
+ * all in fp32 (y from the fp32 value of out), rounded once when stored.  block may be
+ * a slice that fm_gemm_rs filled (fp32); y is the 16-bit input of fm_ag_gemm, or the
+ * 8-bit one of fm_gemm_i8.
+ *   dt         FM_F16 or FM_BF16: y, bias, w and b.
+ *   stream_dt  resid and out: dt or FM_F32.   block_dt  block: dt or FM_F32.
+ *   M, N       rows and row length; N a multiple of 8, at most 16384.
+ *   block      [M, N] or NULL: nothing is added (bias must be NULL and p 0).
+ *   resid      [M, N] or NULL: 0.  Not both NULL.
+ *   bias       [N] or NULL: 0.
+ *   w          [N], or NULL: no norm.  y is NULL if and only if w is.
+ *   b          [N] or NULL: 0; only with w.
+ *   p, rng, draw, row_begin  as fm_dropout (columns from 0).
+ *   out        [M, N] or NULL (not wanted); it may be resid itself.
+ *   y_scale    fp32 [M]: y is int8, its rows as fm_quant_i8 makes them of the fp32
+ *              values.  NULL: y is in dt.
+ *   mean, rstd fp32 [M] or NULL, which the backward needs; only with w.
+ */
+fm_status_t fm_layer_norm(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t block_dt, int64_t M,
+                          int64_t N, const void* block, const void* resid, const void* bias,
+                          const void* w, const void* b, float p, const uint64_t* rng,
+                          int64_t draw, int64_t row_begin, float eps, void* out, void* y,
+                          float* y_scale, float* mean, float* rstd, hipStream_t stream);
+
+/*
+ * fm_layer_norm_bwd -- gradients of fm_layer_norm.
+ *   d_y      [M, N] dt, gradient of y; NULL if and only if w is.
+ *   d_out    [M, N] stream_dt, gradient of out from its later uses, or NULL: 0
+ *            (without w it is needed).
+ *   out      [M, N] stream_dt, and mean, rstd, as the forward stored them; needed with w.
+ *   p, rng, draw, row_begin  as in the forward.
+ *   d_resid  [M, N] stream_dt or NULL: gradient of resid (of out in total).
+ *            It may be d_out itself.
+ *   d_block  [M, N] block_dt or NULL.
+ *   d_bias, d_w, d_b  fp32 [N], written whole, or NULL; d_w and d_b only with w.
+ *   ws, ws_bytes  scratch of fm_layer_norm_workspace_bytes, 16-byte aligned, without
+ *            preparation; needed if any of these three is wanted, one for each call
+ *            that may run at the same time.
+ * The column sums are taken in a fixed order: identical bits on every call.
+ */
+size_t fm_layer_norm_workspace_bytes(int64_t M, int64_t N);
+
+fm_status_t fm_layer_norm_bwd(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t block_dt, int64_t M,
+                              int64_t N, const void* d_y, const void* d_out, const void* out,
+                              const float* mean, const float* rstd, const void* w, float p,
+                              const uint64_t* rng, int64_t draw, int64_t row_begin,
+                              void* d_resid, void* d_block, float* d_bias, float* d_w,
+                              float* d_b, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * 8-bit integers.  fm_quant_i8 -- rows in 8 bits with a scale each: with
+ * top = max |x[i, :]|,
+ *   scale[i] = top / 127     q[i, j] = 127 x[i, j] / top, rounded to nearest even,
+ * so x[i, j] is about q[i, j] * scale[i].  A row whose top is below 2^-100 is held as
+ * zeros with scale 0; one that holds a NaN, or whose top is 2^120 or more, as zeros
+ * with scale NaN (a row of NaN, not of wrong numbers, in what is made of it).
+ * Activations have a row for each token; a weight matrix [N, K] has a row, and so a
+ * scale, for each output channel.
+ *   dt  FM_F16, FM_BF16 or FM_F32: x [M, N];  q int8 [M, N];  scale fp32 [M].
+ */
+fm_status_t fm_quant_i8(fm_dtype_t dt, int64_t M, int64_t N, const void* x, int8_t* q,
+                        float* scale, hipStream_t stream);
+
+/*
+ * fm_gemm_i8 -- product of 8-bit rows:
+ *   C[m, n] = act(a_scale[m] * w_scale[n] * sum_k A[m, k] * W[n, k] + bias[n]).
+ * The sum is exact (32-bit integers); scales, bias and activation are applied in fp32
+ * and the result is rounded once.
+ *   dt       FM_F16 or FM_BF16: bias;  c  dt or FM_F32: C.
+ *   A        int8 [M, K] with a_scale fp32 [M];  W  int8 [N, K] (an output channel's
+ *            weights in a row) with w_scale fp32 [N].  -128 may occur.
+ *   bias     [N] or NULL: 0.   act  fm_act_t.   C  [M, N].
+ *   K a multiple of 16, at most 131056 (the sums fit 32 bits); N a multiple of 8;
+ *   w_scale 16-byte aligned.
+ */
+fm_status_t fm_gemm_i8(fm_dtype_t dt, fm_dtype_t c, int64_t M, int64_t N, int64_t K,
+                       const int8_t* A, const float* a_scale, const int8_t* W,
+                       const float* w_scale, const void* bias, fm_act_t act, void* C,
+                       hipStream_t stream);
+
+/*
+ * fm_linear_i8 -- fm_quant_i8 of the rows of X, then fm_gemm_i8: a linear layer with
+ * 8-bit weights on 16-bit activations, the same bits as those two calls.
+ *   X   [M, K] in dt.   ws, ws_bytes  scratch of fm_linear_i8_workspace_bytes, 16-byte
+ *       aligned, without preparation; one for each call that may run at the same time.
+ */
+size_t fm_linear_i8_workspace_bytes(int64_t M, int64_t K);
+
+fm_status_t fm_linear_i8(fm_dtype_t dt, fm_dtype_t c, int64_t M, int64_t N, int64_t K,
+                         const void* X, const int8_t* W, const float* w_scale, const void* bias,
+                         fm_act_t act, void* C, void* ws, size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -30,7 +30,9 @@ EXPORTS = ("fm_version", "fm_status_str", "fm_gemm", "fm_ag_gemm", "fm_ag_gemm_p
            "fm_moe_gate_workspace_bytes", "fm_moe_gate", "fm_moe_gate_bwd",
            "fm_norm_residual", "fm_norm_residual_workspace_bytes", "fm_norm_residual_bwd",
            "fm_w4_row_bytes", "fm_w4_pack", "fm_gemm_w4", "fm_moe_gather_gemm_w4",
-           "fm_moe_w4_workspace_bytes", "fm_moe_gemm_scatter_w4")
+           "fm_moe_w4_workspace_bytes", "fm_moe_gemm_scatter_w4",
+           "fm_dropout", "fm_layer_norm", "fm_layer_norm_workspace_bytes", "fm_layer_norm_bwd",
+           "fm_quant_i8", "fm_gemm_i8", "fm_linear_i8_workspace_bytes", "fm_linear_i8")
 
 # fm_act_t: activation of MoE layer 0's result (fm_moe_gather_gemm_act)
 FM_ACT_NONE, FM_ACT_RELU, FM_ACT_GELU_TANH, FM_ACT_SILU = 0, 1, 2, 3
@@ -140,6 +142,26 @@ def lib() -> ctypes.CDLL:
     L.fm_moe_gemm_scatter_w4.restype = ctypes.c_int
     L.fm_moe_gemm_scatter_w4.argtypes = [ctypes.c_int, i64, i64, i64, i32, i32, i32, i32, p, p, p,
                                          p, p, p, p, p, p, p, p, sz, p]
+    L.fm_dropout.restype = ctypes.c_int
+    L.fm_dropout.argtypes = [ctypes.c_int, i64, i64, p, f32, p, i64, i64, i64, p, p]
+    L.fm_layer_norm.restype = ctypes.c_int
+    L.fm_layer_norm.argtypes = [ctypes.c_int] * 3 + [i64, i64, p, p, p, p, p, f32, p, i64, i64, f32,
+                                                     p, p, p, p, p, p]
+    L.fm_layer_norm_workspace_bytes.restype = sz
+    L.fm_layer_norm_workspace_bytes.argtypes = [i64, i64]
+    L.fm_layer_norm_bwd.restype = ctypes.c_int
+    L.fm_layer_norm_bwd.argtypes = [ctypes.c_int] * 3 + [i64, i64, p, p, p, p, p, p, f32, p, i64,
+                                                         i64, p, p, p, p, p, p, sz, p]
+    L.fm_quant_i8.restype = ctypes.c_int
+    L.fm_quant_i8.argtypes = [ctypes.c_int, i64, i64, p, p, p, p]
+    L.fm_gemm_i8.restype = ctypes.c_int
+    L.fm_gemm_i8.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, p, p, p, p, p, ctypes.c_int,
+                             p, p]
+    L.fm_linear_i8_workspace_bytes.restype = sz
+    L.fm_linear_i8_workspace_bytes.argtypes = [i64, i64]
+    L.fm_linear_i8.restype = ctypes.c_int
+    L.fm_linear_i8.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, p, p, p, p, ctypes.c_int, p,
+                               p, sz, p]
     _lib = L
     return L
 
@@ -678,3 +700,103 @@ def fm_moe_gemm_scatter_w4(H, packed, scales, topk_ids, sorted_pairs, expert_off
                                         topk_weights, out, expert_begin, group, ws, zeros, add)
     if st:
         raise FluxMIError("fm_moe_gemm_scatter_w4", st)
+
+
+# -- in a dense block: dropout, layer norm, 8-bit products --------------------------
+#
+# rng: int64 [2] on the GPU, seed and offset, read when a kernel runs.  draw numbers
+# the places of a program that draw; forward and backward of one place share it.
+
+def fm_dropout(x, y, p: float, rng, draw: int = 0, row_begin: int = 0, col_begin: int = 0,
+               stream=None) -> None:
+    """y = x / (1 - p) where kept, 0 elsewhere; the backward is the same call on the
+    gradient.  y may be x."""
+    rt = _rt()
+    d = rt.device()
+    st = rt.native.dropout(d, rt.stream(d) if stream is None else stream.cuda_stream, x, y, p, rng,
+                           draw, row_begin, col_begin)
+    if st:
+        raise FluxMIError("fm_dropout", st)
+
+
+def fm_layer_norm(out, y, block=None, resid=None, bias=None, w=None, b=None, p: float = 0.0,
+                  rng=None, draw: int = 0, row_begin: int = 0, eps: float = 1e-5, y_scale=None,
+                  mean=None, rstd=None, stream=None) -> None:
+    """out = resid + dropout(block + bias), y = (out - mean) * rstd * w + b; out or y
+    may be None (not wanted), as may every operand (see fluxmi.h).  With y_scale [M], y
+    is int8."""
+    if (block is None and resid is None) or (out is None and y is None):
+        raise ValueError("fm_layer_norm: block or resid, and out or y, are needed")
+    rt = _rt()
+    d = rt.device()
+    st = rt.native.layer_norm(d, rt.stream(d) if stream is None else stream.cuda_stream, out, y,
+                              block, resid, bias, w, b, p, rng, draw, row_begin, eps, y_scale,
+                              mean, rstd)
+    if st:
+        raise FluxMIError("fm_layer_norm", st)
+
+
+def fm_layer_norm_workspace_bytes(M: int, N: int) -> int:
+    """Bytes of scratch that fm_layer_norm_bwd needs for its column sums."""
+    return int(lib().fm_layer_norm_workspace_bytes(int(M), int(N)))
+
+
+def layer_norm_workspace(M: int, N: int, device="cuda:0"):
+    """A uint8 device tensor of fm_layer_norm_workspace_bytes bytes."""
+    return _scratch("fm_layer_norm_workspace_bytes", fm_layer_norm_workspace_bytes(M, N), device)
+
+
+def fm_layer_norm_bwd(d_resid, d_block, out=None, d_y=None, d_out=None, w=None, p: float = 0.0,
+                      rng=None, draw: int = 0, row_begin: int = 0, mean=None, rstd=None,
+                      d_bias=None, d_w=None, d_b=None, ws=None, stream=None) -> None:
+    """Gradients of fm_layer_norm; each of d_resid, d_block, d_bias, d_w and d_b may be
+    None (not wanted)."""
+    if d_y is None and d_out is None:
+        raise ValueError("fm_layer_norm_bwd: d_y or d_out is needed")
+    rt = _rt()
+    d = rt.device()
+    st = rt.native.layer_norm_bwd(d, rt.stream(d) if stream is None else stream.cuda_stream,
+                                  d_resid, d_block, out, d_y, d_out, w, p, rng, draw, row_begin,
+                                  mean, rstd, d_bias, d_w, d_b, ws)
+    if st:
+        raise FluxMIError("fm_layer_norm_bwd", st)
+
+
+def fm_quant_i8(x, q, scale, stream=None) -> None:
+    """Rows of x [M, N] as int8 q with a scale [M] each."""
+    rt = _rt()
+    d = rt.device()
+    st = rt.native.quant_i8(d, rt.stream(d) if stream is None else stream.cuda_stream, x, q, scale)
+    if st:
+        raise FluxMIError("fm_quant_i8", st)
+
+
+def fm_gemm_i8(A, a_scale, W, w_scale, C, bias=None, act: int = FM_ACT_NONE, stream=None) -> None:
+    """C = act(a_scale * w_scale * (A @ W.T) + bias), A int8 [M, K], W int8 [N, K]."""
+    rt = _rt()
+    d = rt.device()
+    st = rt.native.gemm_i8(d, rt.stream(d) if stream is None else stream.cuda_stream, A, a_scale,
+                           W, w_scale, C, bias, act)
+    if st:
+        raise FluxMIError("fm_gemm_i8", st)
+
+
+def fm_linear_i8_workspace_bytes(M: int, K: int) -> int:
+    """Bytes of scratch that fm_linear_i8 needs."""
+    return int(lib().fm_linear_i8_workspace_bytes(int(M), int(K)))
+
+
+def linear_i8_workspace(M: int, K: int, device="cuda:0"):
+    """A uint8 device tensor of fm_linear_i8_workspace_bytes bytes."""
+    return _scratch("fm_linear_i8_workspace_bytes", fm_linear_i8_workspace_bytes(M, K), device)
+
+
+def fm_linear_i8(X, W, w_scale, C, bias=None, act: int = FM_ACT_NONE, ws=None, stream=None) -> None:
+    """C = act(X @ (w_scale * W).T + bias) with the rows of X held in 8 bits: fm_quant_i8
+    and fm_gemm_i8 in one call."""
+    rt = _rt()
+    d = rt.device()
+    st = rt.native.linear_i8(d, rt.stream(d) if stream is None else stream.cuda_stream, X, W,
+                             w_scale, C, bias, act, ws)
+    if st:
+        raise FluxMIError("fm_linear_i8", st)

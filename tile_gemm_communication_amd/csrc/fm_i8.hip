@@ -1,0 +1,230 @@
+// fm_i8.hip -- rows in 8 bits with a scale each, and their products with 8-bit
+// weights that have a scale for each output channel.
+#include <algorithm>
+
+#include "fm_act.hpp"
+#include "fm_layer_norm.hpp"
+
+namespace fm {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// -- rows to 8 bits ------------------------------------------------------------
+
+constexpr int kQuantLanes = 256;
+constexpr int kQuantHeld = 4;   // chunks of eight elements that a lane keeps between its passes
+
+struct QuantArgs {
+  const void* x;
+  char* q;
+  float* scale;
+  int64_t M, N;
+};
+
+// One row a block: the largest magnitude, then the values, from registers as far as
+// they fit and read again beyond.
+template <typename E>
+__global__ __launch_bounds__(kQuantLanes) void quant_rows(const QuantArgs a) {
+  using T = typename Elem<E>::type;
+  __shared__ uint32_t s_top[kQuantLanes / 64];
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= a.M) return;
+  const T* x = static_cast<const T*>(a.x) + row * a.N;
+  f32x4 v[kQuantHeld][2];
+  uint32_t top = 0;
+  auto join = [&](const f32x4 (&w)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, magnitude(w[h][i]));
+  };
+#pragma unroll
+  for (int c = 0; c < kQuantHeld; ++c) {
+    const int64_t e = (int64_t)(c * kQuantLanes + threadIdx.x) * 8;
+    if (e < a.N) {
+      load8<E>(x + e, v[c]);
+      join(v[c]);
+    }
+  }
+  const int64_t rest = (int64_t)(kQuantHeld * kQuantLanes + threadIdx.x) * 8;
+  for (int64_t e = rest; e < a.N; e += kQuantLanes * 8) {
+    f32x4 w[2];
+    load8<E>(x + e, w);
+    join(w);
+  }
+  const RowQuant r = row_quant(row_umax<kQuantLanes>(top, s_top));
+  if (threadIdx.x == 0) a.scale[row] = r.scale;
+  char* q = a.q + row * a.N;
+  auto put = [&](int64_t e, const f32x4 (&w)[2]) {
+    *reinterpret_cast<u32x2*>(q + e) = u32x2{quant4(w[0], r), quant4(w[1], r)};
+  };
+#pragma unroll
+  for (int c = 0; c < kQuantHeld; ++c) {
+    const int64_t e = (int64_t)(c * kQuantLanes + threadIdx.x) * 8;
+    if (e < a.N) put(e, v[c]);
+  }
+  for (int64_t e = rest; e < a.N; e += kQuantLanes * 8) {
+    f32x4 w[2];
+    load8<E>(x + e, w);
+    put(e, w);
+  }
+}
+
+fm_status_t check_quant(fm_dtype_t dt, int64_t M, int64_t N) {
+  if (dt != FM_F16 && dt != FM_BF16 && dt != FM_F32) return FM_ERR_UNSUPPORTED;
+  if (M < 0 || N < 0 || N % 8) return FM_ERR_INVALID_ARG;
+  if (M >= (1ll << 31) || N >= (1ll << 31)) return FM_ERR_UNSUPPORTED;
+  return FM_OK;
+}
+
+void launch_quant(fm_dtype_t dt, const QuantArgs& a, hipStream_t stream) {
+  const int64_t x = std::min<int64_t>(a.M, 1 << 20);
+  const dim3 grid((unsigned)x, (unsigned)cdiv(a.M, x)), lanes(kQuantLanes);
+  if (dt == FM_F16) hipLaunchKernelGGL(quant_rows<F16>, grid, lanes, 0, stream, a);
+  else if (dt == FM_BF16) hipLaunchKernelGGL(quant_rows<BF16>, grid, lanes, 0, stream, a);
+  else hipLaunchKernelGGL(quant_rows<F32>, grid, lanes, 0, stream, a);
+}
+
+// -- products --------------------------------------------------------------------
+
+struct I8Args {
+  const char *A, *W;                // [M, K], [N, K]
+  const float *a_scale, *w_scale;   // [M], [N]
+  const void* bias;                 // [N] or NULL
+  char* C;                          // [M, N]
+  int64_t M, N, K;
+  int act;
+};
+
+// Four neighbouring results of row m from column n on: the sums' scales, bias,
+// activation, rounding.
+template <typename E, typename O>
+__device__ __forceinline__ void finish4(const I8Args& a, int64_t m, int64_t n, i32x4 sum, float sa) {
+  const f32x4 sw = *reinterpret_cast<const f32x4*>(a.w_scale + n);
+  f32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (float)sum[i] * (sa * sw[i]);
+  if (a.bias) v += load4<E>(static_cast<const typename Elem<E>::type*>(a.bias) + n);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = activate(v[i], a.act);
+  store4<O>(reinterpret_cast<typename Elem<O>::type*>(a.C) + m * a.N + n, v);
+}
+
+// A block of four waves takes 64 x 64 results, a wave 32 x 32 straight from memory.
+template <typename E, typename O>
+__global__ __launch_bounds__(256) void gemm_i8_simple(const I8Args a) {
+  const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
+  const int64_t n0 = (int64_t)blockIdx.x * 64 + (w & 1) * 32;
+  const int64_t m0 = (int64_t)blockIdx.y * 64 + (w >> 1) * 32;
+  if (m0 >= a.M || n0 >= a.N) return;
+  const int r = lane & 31, half = lane >> 5;
+  const int64_t m = m0 + r, n = n0 + r;
+  const char* pa = a.A + min(m, a.M - 1) * a.K + half * 16;
+  const char* pw = a.W + min(n, a.N - 1) * a.K + half * 16;
+  i32x16 acc = {};
+  for (int64_t k = 0; k < a.K; k += 32) {
+    i32x4 x = {}, y = {};
+    if (k + half * 16 < a.K) {
+      x = *reinterpret_cast<const i32x4*>(pa + k);
+      y = *reinterpret_cast<const i32x4*>(pw + k);
+    }
+    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(y, x, acc, 0, 0, 0);
+  }
+  if (m >= a.M) return;
+  const float sa = a.a_scale[m];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t c = n0 + 8 * q + 4 * half;
+    if (c < a.N)
+      finish4<E, O>(a, m, c, i32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]}, sa);
+  }
+}
+
+// A sum of K products of bytes fits 32 bits up to here (127 * 128 * K, and -128 may
+// stand in a caller's own codes: 2^14 K < 2^31).
+constexpr int64_t kI8MaxK = (1ll << 17) - 16;
+constexpr int64_t kI8MaxDim = 1ll << 22;
+
+fm_status_t check_i8(fm_dtype_t dt, fm_dtype_t c, int64_t M, int64_t N, int64_t K, fm_act_t act) {
+  if ((dt != FM_F16 && dt != FM_BF16) || (c != dt && c != FM_F32)) return FM_ERR_UNSUPPORTED;
+  if (M < 0 || N < 0 || K < 0 || N % 8 || K % 16) return FM_ERR_INVALID_ARG;
+  if ((int)act < FM_ACT_NONE || (int)act > FM_ACT_SILU) return FM_ERR_INVALID_ARG;
+  if (M >= kI8MaxDim || N >= kI8MaxDim || K > kI8MaxK) return FM_ERR_UNSUPPORTED;
+  return FM_OK;
+}
+
+template <typename E, typename O>
+void launch_gemm(const I8Args& a, hipStream_t stream) {
+  hipLaunchKernelGGL((gemm_i8_simple<E, O>), dim3((unsigned)cdiv(a.N, 64), (unsigned)cdiv(a.M, 64)),
+                     dim3(256), 0, stream, a);
+}
+
+void launch_gemm_types(fm_dtype_t dt, fm_dtype_t c, const I8Args& a, hipStream_t stream) {
+  if (dt == FM_F16) {
+    if (c == FM_F32) launch_gemm<F16, F32>(a, stream);
+    else launch_gemm<F16, F16>(a, stream);
+  } else {
+    if (c == FM_F32) launch_gemm<BF16, F32>(a, stream);
+    else launch_gemm<BF16, BF16>(a, stream);
+  }
+}
+
+int64_t codes_bytes(int64_t M, int64_t K) { return cdiv(M * K, 256) * 256; }
+
+}  // namespace
+}  // namespace fm
+
+using namespace fm;
+
+extern "C" fm_status_t fm_quant_i8(fm_dtype_t dt, int64_t M, int64_t N, const void* x, int8_t* q,
+                                   float* scale, hipStream_t stream) {
+  const fm_status_t st = check_quant(dt, M, N);
+  if (st != FM_OK) return st;
+  if (M == 0) return FM_OK;
+  if (!scale || !aligned4(scale)) return FM_ERR_INVALID_ARG;
+  if (N > 0 && (!x || !q)) return FM_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q)) return FM_ERR_INVALID_ARG;
+  launch_quant(dt, {x, reinterpret_cast<char*>(q), scale, M, N}, stream);
+  return launch_status();
+}
+
+extern "C" fm_status_t fm_gemm_i8(fm_dtype_t dt, fm_dtype_t c, int64_t M, int64_t N, int64_t K,
+                                  const int8_t* A, const float* a_scale, const int8_t* W,
+                                  const float* w_scale, const void* bias, fm_act_t act, void* C,
+                                  hipStream_t stream) {
+  const fm_status_t st = check_i8(dt, c, M, N, K, act);
+  if (st != FM_OK) return st;
+  if (M == 0 || N == 0) return FM_OK;
+  if (!a_scale || !w_scale || !C || (K > 0 && (!A || !W))) return FM_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)A, (const void*)W, (const void*)w_scale, bias, (const void*)C})
+    if (!aligned16(p)) return FM_ERR_INVALID_ARG;
+  if (!aligned4(a_scale)) return FM_ERR_INVALID_ARG;
+  launch_gemm_types(dt, c, {(const char*)A, (const char*)W, a_scale, w_scale, bias, (char*)C, M, N, K, (int)act},
+                    stream);
+  return launch_status();
+}
+
+extern "C" size_t fm_linear_i8_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 0 || K < 0 || K % 16 || M >= kI8MaxDim || K > kI8MaxK) return 0;
+  return std::max<size_t>((size_t)codes_bytes(M, K) + (size_t)M * 4, 256);
+}
+
+extern "C" fm_status_t fm_linear_i8(fm_dtype_t dt, fm_dtype_t c, int64_t M, int64_t N, int64_t K,
+                                    const void* X, const int8_t* W, const float* w_scale,
+                                    const void* bias, fm_act_t act, void* C, void* ws,
+                                    size_t ws_bytes, hipStream_t stream) {
+  const fm_status_t st = check_i8(dt, c, M, N, K, act);
+  if (st != FM_OK) return st;
+  if (M == 0 || N == 0) return FM_OK;
+  if (!w_scale || !C || (K > 0 && (!X || !W))) return FM_ERR_INVALID_ARG;
+  for (const void* p : {X, (const void*)W, (const void*)w_scale, bias, (const void*)C, (const void*)ws})
+    if (!aligned16(p)) return FM_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < fm_linear_i8_workspace_bytes(M, K)) return FM_ERR_INVALID_ARG;
+  char* codes = static_cast<char*>(ws);
+  float* scale = reinterpret_cast<float*>(codes + codes_bytes(M, K));
+  launch_quant(dt, {X, codes, scale, M, K}, stream);
+  launch_gemm_types(dt, c, {codes, (const char*)W, scale, w_scale, bias, (char*)C, M, N, K, (int)act}, stream);
+  return launch_status();
+}

@@ -370,6 +370,143 @@ PyObject* moe_gemm_scatter_w4(PyObject*, PyObject* const* v, Py_ssize_t n) {
                                         (float*)po, ws, bytes, stream));
 }
 
+// The random state of a call that drops: seed and offset.
+const uint64_t* rng_of(Call& c, PyObject* o) { return (const uint64_t*)c.at("rng", o, at::kLong, {2}); }
+
+// device, stream, x, y, p, rng, draw, row_begin, col_begin
+PyObject* dropout(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (!count(n, 9)) return nullptr;
+  const Args a{v};
+  Call c{"fm_dropout", (int)a.i(0)};
+  const at::Tensor* x = c.matrix("x", v[2]);
+  if (c.bad) return nullptr;
+  const int64_t M = x->size(0), N = x->size(1);
+  const at::ScalarType dt = x->scalar_type();
+  const fm_dtype_t code = c.code(dt);
+  void *px = c.at("x", v[2], dt, {M, N}), *py = c.at("y", v[3], dt, {M, N});
+  const uint64_t* rng = rng_of(c, v[5]);
+  const float p = a.f(4);
+  const int64_t draw = a.i(6), row = a.i(7), col = a.i(8);
+  const hipStream_t stream = a.stream(1);
+  if (c.bad || PyErr_Occurred()) return nullptr;
+  return done(c, fm_dropout(code, M, N, px, p, rng, draw, row, col, py, stream));
+}
+
+// device, stream, out, y, block, resid, bias, w, b, p, rng, draw, row_begin, eps,
+// y_scale, mean, rstd
+PyObject* layer_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (!count(n, 17)) return nullptr;
+  const Args a{v};
+  Call c{"fm_layer_norm", (int)a.i(0)};
+  const at::Tensor* like = c.matrix("block or resid", v[4] != Py_None ? v[4] : v[5]);
+  if (c.bad) return nullptr;
+  const int64_t M = like->size(0), N = like->size(1);
+  const NormTypes t(c, v, {7, 6, 8}, {5, 2}, {4});
+  void *pb = c.at("block", v[4], t.bd, {M, N}), *pr = c.at("resid", v[5], t.sd, {M, N}),
+       *pi = c.at("bias", v[6], t.dt, {N}), *pw = c.at("w", v[7], t.dt, {N}),
+       *pc = c.at("b", v[8], t.dt, {N}), *po = c.at("out", v[2], t.sd, {M, N}),
+       *py = c.at("y", v[3], v[14] == Py_None ? t.dt : at::kChar, {M, N}),
+       *ps = c.at("y_scale", v[14], kFloat, {M}), *pm = c.at("mean", v[15], kFloat, {M}),
+       *pq = c.at("rstd", v[16], kFloat, {M});
+  const uint64_t* rng = rng_of(c, v[10]);
+  const fm_dtype_t dt = c.code(t.dt), sd = c.code(t.sd), bd = c.code(t.bd);
+  const float p = a.f(9), eps = a.f(13);
+  const int64_t draw = a.i(11), row = a.i(12);
+  const hipStream_t stream = a.stream(1);
+  if (c.bad || PyErr_Occurred()) return nullptr;
+  return done(c, fm_layer_norm(dt, sd, bd, M, N, pb, pr, pi, pw, pc, p, rng, draw, row, eps, po, py,
+                               (float*)ps, (float*)pm, (float*)pq, stream));
+}
+
+// device, stream, d_resid, d_block, out, d_y, d_out, w, p, rng, draw, row_begin, mean,
+// rstd, d_bias, d_w, d_b, ws
+PyObject* layer_norm_bwd(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (!count(n, 18)) return nullptr;
+  const Args a{v};
+  Call c{"fm_layer_norm_bwd", (int)a.i(0)};
+  const at::Tensor* like = c.matrix("d_y or d_out", v[5] != Py_None ? v[5] : v[6]);
+  if (c.bad) return nullptr;
+  const int64_t M = like->size(0), N = like->size(1);
+  const NormTypes t(c, v, {5, 7}, {6, 4, 2}, {3});
+  size_t bytes;
+  void* ws = c.workspace(v[17], bytes);
+  void *dr = c.at("d_resid", v[2], t.sd, {M, N}), *db = c.at("d_block", v[3], t.bd, {M, N}),
+       *po = c.at("out", v[4], t.sd, {M, N}), *dy = c.at("d_y", v[5], t.dt, {M, N}),
+       *dz = c.at("d_out", v[6], t.sd, {M, N}), *pw = c.at("w", v[7], t.dt, {N}),
+       *pm = c.at("mean", v[12], kFloat, {M}), *pq = c.at("rstd", v[13], kFloat, {M}),
+       *di = c.at("d_bias", v[14], kFloat, {N}), *dw = c.at("d_w", v[15], kFloat, {N}),
+       *dc = c.at("d_b", v[16], kFloat, {N});
+  const uint64_t* rng = rng_of(c, v[9]);
+  const fm_dtype_t dt = c.code(t.dt), sd = c.code(t.sd), bd = c.code(t.bd);
+  const float p = a.f(8);
+  const int64_t draw = a.i(10), row = a.i(11);
+  const hipStream_t stream = a.stream(1);
+  if (c.bad || PyErr_Occurred()) return nullptr;
+  return done(c, fm_layer_norm_bwd(dt, sd, bd, M, N, dy, dz, po, (const float*)pm,
+                                   (const float*)pq, pw, p, rng, draw, row, dr, db, (float*)di,
+                                   (float*)dw, (float*)dc, ws, bytes, stream));
+}
+
+// device, stream, x, q, scale
+PyObject* quant_i8(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (!count(n, 5)) return nullptr;
+  const Args a{v};
+  Call c{"fm_quant_i8", (int)a.i(0)};
+  const at::Tensor* x = c.matrix("x", v[2]);
+  if (c.bad) return nullptr;
+  const int64_t M = x->size(0), N = x->size(1);
+  const at::ScalarType dt = x->scalar_type();
+  const fm_dtype_t code = c.code(dt);
+  void *px = c.at("x", v[2], dt, {M, N}), *pq = c.at("q", v[3], at::kChar, {M, N}),
+       *ps = c.at("scale", v[4], kFloat, {M});
+  const hipStream_t stream = a.stream(1);
+  if (c.bad || PyErr_Occurred()) return nullptr;
+  return done(c, fm_quant_i8(code, M, N, px, (int8_t*)pq, (float*)ps, stream));
+}
+
+// device, stream, A, a_scale, W, w_scale, C, bias, act
+PyObject* gemm_i8(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (!count(n, 9)) return nullptr;
+  const Args a{v};
+  Call c{"fm_gemm_i8", (int)a.i(0)};
+  const at::Tensor *x = c.matrix("A", v[2]), *y = c.matrix("C", v[6]), *b = c.tensor("bias", v[7]);
+  if (c.bad) return nullptr;
+  const int64_t M = x->size(0), K = x->size(1), N = y->size(1);
+  const at::ScalarType ct = y->scalar_type(),
+                       dt = b ? b->scalar_type() : ct == kFloat ? at::kBFloat16 : ct;
+  const fm_dtype_t code = c.code(dt), cc = c.code(ct);
+  const int32_t act = c.i32("act", v[8]);
+  void *pa = c.at("A", v[2], at::kChar, {M, K}), *ps = c.at("a_scale", v[3], kFloat, {M}),
+       *pw = c.at("W", v[4], at::kChar, {N, K}), *pt = c.at("w_scale", v[5], kFloat, {N}),
+       *pc = c.at("C", v[6], ct, {M, N}), *pb = c.at("bias", v[7], dt, {N});
+  const hipStream_t stream = a.stream(1);
+  if (c.bad || PyErr_Occurred()) return nullptr;
+  return done(c, fm_gemm_i8(code, cc, M, N, K, (const int8_t*)pa, (const float*)ps,
+                            (const int8_t*)pw, (const float*)pt, pb, (fm_act_t)act, pc, stream));
+}
+
+// device, stream, X, W, w_scale, C, bias, act, ws
+PyObject* linear_i8(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (!count(n, 9)) return nullptr;
+  const Args a{v};
+  Call c{"fm_linear_i8", (int)a.i(0)};
+  const at::Tensor *x = c.matrix("X", v[2]), *y = c.matrix("C", v[5]);
+  if (c.bad) return nullptr;
+  const int64_t M = x->size(0), K = x->size(1), N = y->size(1);
+  const at::ScalarType dt = x->scalar_type(), ct = y->scalar_type();
+  const fm_dtype_t code = c.code(dt), cc = c.code(ct);
+  const int32_t act = c.i32("act", v[7]);
+  size_t bytes;
+  void* ws = c.workspace(v[8], bytes);
+  void *px = c.at("X", v[2], dt, {M, K}), *pw = c.at("W", v[3], at::kChar, {N, K}),
+       *pt = c.at("w_scale", v[4], kFloat, {N}), *pc = c.at("C", v[5], ct, {M, N}),
+       *pb = c.at("bias", v[6], dt, {N});
+  const hipStream_t stream = a.stream(1);
+  if (c.bad || PyErr_Occurred()) return nullptr;
+  return done(c, fm_linear_i8(code, cc, M, N, K, px, (const int8_t*)pw, (const float*)pt, pb,
+                              (fm_act_t)act, pc, ws, bytes, stream));
+}
+
 // No C++ exception leaves the module.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* v, Py_ssize_t n) {
@@ -389,6 +526,12 @@ PyMethodDef methods[] = {FM_METHOD(moe_gate),
                          FM_METHOD(gemm_w4),
                          FM_METHOD(moe_gather_gemm_w4),
                          FM_METHOD(moe_gemm_scatter_w4),
+                         FM_METHOD(dropout),
+                         FM_METHOD(layer_norm),
+                         FM_METHOD(layer_norm_bwd),
+                         FM_METHOD(quant_i8),
+                         FM_METHOD(gemm_i8),
+                         FM_METHOD(linear_i8),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fluxmi", nullptr, -1, methods};
 

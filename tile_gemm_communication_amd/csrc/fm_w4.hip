@@ -27,6 +27,7 @@
 // fused multiply-adds a product), use LDS in 38% and the matrix core in 16%.
 #include <algorithm>
 
+#include "fm_act.hpp"
 #include "fm_w4_index.hpp"
 #include "fm_wave.hpp"
 
@@ -122,19 +123,6 @@ struct W4Args {
   int32_t *pairs_out, *offsets_out;
   int n_pairs, e0;
 };
-
-__device__ __forceinline__ float activate(float x, int act) {
-  switch (act) {
-    case FM_ACT_RELU: return x > 0.f ? x : 0.f;
-    case FM_ACT_GELU_TANH: {
-      // x/2 (1 + tanh u) = x / (1 + exp(-2u))
-      const float u = 0.7978845608028654f * (x + 0.044715f * x * x * x);
-      return x / (1.f + __expf(-2.f * u));
-    }
-    case FM_ACT_SILU: return x / (1.f + __expf(-x));
-    default: return x;
-  }
-}
 
 // The column tile of a block: each XCD (blocks go to them in turn) takes
 // neighbouring tiles, whose scales share cache lines.

@@ -80,6 +80,8 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 // Element types of a row: F32 beside the 16-bit formats.
 struct F32 {
   static constexpr fm_dtype_t id = FM_F32;
