@@ -1,6 +1,8 @@
 // fm_act.hpp -- activations of a product's epilogue (fm_act_t).
 #pragma once
 
+#include <type_traits>
+
 #include "fm_common.hpp"
 
 namespace fm {
@@ -15,6 +17,23 @@ __device__ __forceinline__ float activate(float x, int act) {
     }
     case FM_ACT_SILU: return x / (1.f + __expf(-x));
     default: return x;
+  }
+}
+
+// The same of N values, one branch for all.
+template <int N>
+__device__ __forceinline__ void activate_all(f32x4 (&v)[N], int act) {
+  auto each = [&](auto code) {
+#pragma unroll
+    for (int h = 0; h < N; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[h][i] = activate(v[h][i], decltype(code)::value);
+  };
+  switch (act) {
+    case FM_ACT_RELU: return each(std::integral_constant<int, FM_ACT_RELU>{});
+    case FM_ACT_GELU_TANH: return each(std::integral_constant<int, FM_ACT_GELU_TANH>{});
+    case FM_ACT_SILU: return each(std::integral_constant<int, FM_ACT_SILU>{});
+    default: return;
   }
 }
 

@@ -1,15 +1,15 @@
 // fm_i8.hip -- rows in 8 bits with a scale each, and their products with 8-bit
 // weights that have a scale for each output channel.
 #include <algorithm>
+#include <cstdlib>
 
 #include "fm_act.hpp"
+#include "fm_i8_tile.hpp"
 #include "fm_layer_norm.hpp"
+#include "fm_sched.hpp"
 
 namespace fm {
 namespace {
-
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // -- rows to 8 bits ------------------------------------------------------------
 
@@ -96,49 +96,83 @@ struct I8Args {
   char* C;                          // [M, N]
   int64_t M, N, K;
   int act;
+  int tiles_m, tiles_n, group_m;
 };
 
-// Four neighbouring results of row m from column n on: the sums' scales, bias,
-// activation, rounding.
-template <typename E, typename O>
-__device__ __forceinline__ void finish4(const I8Args& a, int64_t m, int64_t n, i32x4 sum, float sa) {
-  const f32x4 sw = *reinterpret_cast<const f32x4*>(a.w_scale + n);
-  f32x4 v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = (float)sum[i] * (sa * sw[i]);
-  if (a.bias) v += load4<E>(static_cast<const typename Elem<E>::type*>(a.bias) + n);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = activate(v[i], a.act);
-  store4<O>(reinterpret_cast<typename Elem<O>::type*>(a.C) + m * a.N + n, v);
+// Eight results of a row from column n on: the sums' scales, bias, activation, rounding.
+struct Columns {
+  f32x4 scale[2], bias[2];
+};
+
+template <typename E>
+__device__ __forceinline__ Columns columns(const I8Args& a, int64_t n) {
+  Columns c = {};
+  load8<F32>(a.w_scale + n, c.scale);
+  if (a.bias) load8<E>(static_cast<const typename Elem<E>::type*>(a.bias) + n, c.bias);
+  return c;
 }
 
-// A block of four waves takes 64 x 64 results, a wave 32 x 32 straight from memory.
-template <typename E, typename O>
-__global__ __launch_bounds__(256) void gemm_i8_simple(const I8Args a) {
-  const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
-  const int64_t n0 = (int64_t)blockIdx.x * 64 + (w & 1) * 32;
-  const int64_t m0 = (int64_t)blockIdx.y * 64 + (w >> 1) * 32;
-  if (m0 >= a.M || n0 >= a.N) return;
-  const int r = lane & 31, half = lane >> 5;
-  const int64_t m = m0 + r, n = n0 + r;
-  const char* pa = a.A + min(m, a.M - 1) * a.K + half * 16;
-  const char* pw = a.W + min(n, a.N - 1) * a.K + half * 16;
-  i32x16 acc = {};
-  for (int64_t k = 0; k < a.K; k += 32) {
-    i32x4 x = {}, y = {};
-    if (k + half * 16 < a.K) {
-      x = *reinterpret_cast<const i32x4*>(pa + k);
-      y = *reinterpret_cast<const i32x4*>(pw + k);
-    }
-    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(y, x, acc, 0, 0, 0);
-  }
-  if (m >= a.M) return;
-  const float sa = a.a_scale[m];
+template <typename O>
+__device__ __forceinline__ void finish8(const I8Args& a, const Columns& c, const i32x4 (&sum)[2], float sa,
+                                        int64_t at) {
+  f32x4 v[2];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t c = n0 + 8 * q + 4 * half;
-    if (c < a.N)
-      finish4<E, O>(a, m, c, i32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]}, sa);
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[h][i] = (float)sum[h][i] * (sa * c.scale[h][i]) + c.bias[h][i];
+  activate_all(v, a.act);
+  store8<O>(reinterpret_cast<typename Elem<O>::type*>(a.C) + at, v);
+}
+
+// A persistent grid of macro-tiles (fm_sched.hpp's order).  The epilogue turns each
+// 32-row block of a wave around through its own part of LDS, finished and rounded, so
+// that stores cover whole pieces of rows.
+template <typename E, typename O, int BM, int BN, int NSTAGE>
+__global__ __launch_bounds__(256, 1) void gemm_i8_tiles(const I8Args a) {
+  using Tile = I8Tile<BM, BN, NSTAGE>;
+  constexpr int PITCH = Tile::WN * 4 + 16, LPR = Tile::WN / 8;   // staged row, lanes of one
+  static_assert(4 * 32 * PITCH <= Tile::LDS_BYTES && 32 * LPR % 64 == 0, "staging");
+  __shared__ __attribute__((aligned(16))) char smem[Tile::LDS_BYTES];
+  Tile t(smem, a.K);
+  const int r32 = t.lane & 31, hi = t.lane >> 5;
+  char* stage = smem + t.w * 32 * PITCH;
+  const int total = a.tiles_m * a.tiles_n;
+  for (int L = xcd_slot(blockIdx.x, gridDim.x); L < total; L += gridDim.x) {
+    int tm, tn;
+    band_coords(L, a.tiles_m, a.tiles_n, a.group_m, tm, tn);
+    // the operands' bases must sit in scalar registers for the loads
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+    const int rows = (int)min((int64_t)BM, a.M - m0), cols = (int)min((int64_t)BN, a.N - n0);
+    t.set_tile(a.A + m0 * a.K, rows, a.W + n0 * a.K, cols, a.K);
+    t.run();
+    __syncthreads();   // every wave has read its last fragments
+#pragma unroll
+    for (int i = 0; i < Tile::FM; ++i) {
+      asm volatile("" ::: "memory");   // one block's registers after another's
+#pragma unroll
+      for (int j = 0; j < Tile::FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const i32x16& s = t.acc[i][j];
+          *reinterpret_cast<i32x4*>(stage + r32 * PITCH + (32 * j + 8 * r + 4 * hi) * 4) =
+              i32x4{s[4 * r], s[4 * r + 1], s[4 * r + 2], s[4 * r + 3]};
+        }
+      wave_lds_sync();
+#pragma unroll 2
+      for (int q = 0; q < 32 * LPR / 64; ++q) {
+        const int k = q * 64 + t.lane, y = k / LPR, x = k % LPR * 8;
+        const int m = t.wm * Tile::WM + 32 * i + y, n = t.wn * Tile::WN + x;
+        if (m < rows && n < cols) {
+          const i32x4* p = reinterpret_cast<const i32x4*>(stage + y * PITCH + x * 4);
+          const i32x4 sum[2] = {p[0], p[1]};
+          finish8<O>(a, columns<E>(a, n0 + n), sum, a.a_scale[m0 + m], (m0 + m) * a.N + n0 + n);
+        }
+      }
+      wave_lds_sync();
+    }
+    __syncthreads();   // before the next tile's loads land in LDS
   }
 }
 
@@ -155,10 +189,33 @@ fm_status_t check_i8(fm_dtype_t dt, fm_dtype_t c, int64_t M, int64_t N, int64_t 
   return FM_OK;
 }
 
+template <typename E, typename O, int BM, int BN, int NSTAGE>
+void launch_tiles(I8Args a, hipStream_t stream) {
+  a.tiles_m = (int)cdiv(a.M, BM);
+  a.tiles_n = (int)cdiv(a.N, BN);
+  a.group_m = std::min(8, a.tiles_m);
+  const int64_t total = (int64_t)a.tiles_m * a.tiles_n;
+  hipLaunchKernelGGL((gemm_i8_tiles<E, O, BM, BN, NSTAGE>), dim3((unsigned)std::min<int64_t>(total, device_cu_count() * std::min<int>(3, 160 * 1024 / I8Tile<BM, BN, NSTAGE>::LDS_BYTES))),
+                     dim3(256), 0, stream, a);
+}
+
 template <typename E, typename O>
 void launch_gemm(const I8Args& a, hipStream_t stream) {
-  hipLaunchKernelGGL((gemm_i8_simple<E, O>), dim3((unsigned)cdiv(a.N, 64), (unsigned)cdiv(a.M, 64)),
-                     dim3(256), 0, stream, a);
+  const char* v = std::getenv("FM_I8");
+  const int k = v ? std::atoi(v) : 0;
+  if (k == 1) return launch_tiles<E, O, 256, 256, 2>(a, stream);
+  if (k == 2) return launch_tiles<E, O, 256, 192, 2>(a, stream);
+  if (k == 3) return launch_tiles<E, O, 256, 128, 2>(a, stream);
+  if (k == 4) return launch_tiles<E, O, 256, 128, 3>(a, stream);
+  if (k == 5) return launch_tiles<E, O, 128, 128, 3>(a, stream);
+  if (k == 6) return launch_tiles<E, O, 128, 64, 3>(a, stream);
+  if (k == 7) return launch_tiles<E, O, 64, 64, 3>(a, stream);
+  if (k == 8) return launch_tiles<E, O, 192, 256, 2>(a, stream);
+  if (k == 9) return launch_tiles<E, O, 128, 192, 3>(a, stream);
+  if (k == 10) return launch_tiles<E, O, 128, 128, 4>(a, stream);
+  if (k == 11) return launch_tiles<E, O, 64, 64, 5>(a, stream);
+  if (k == 12) return launch_tiles<E, O, 64, 128, 4>(a, stream);
+  return launch_tiles<E, O, 64, 64, 3>(a, stream);
 }
 
 void launch_gemm_types(fm_dtype_t dt, fm_dtype_t c, const I8Args& a, hipStream_t stream) {
