@@ -1,0 +1,181 @@
+// fm_i8_few.hip -- 8-bit products of few rows: the weights stream through once.
+//
+// A block takes 8 C8 columns, as many as make one block a compute unit, and all rows of
+// x; its waves share the sum over k, wave w the 128-byte steps w, w + NWV, ...  Each wave
+// keeps a ring of S steps in its own part of LDS, filled by direct-to-LDS loads of eight
+// whole 128-byte pieces of rows, so that S - 1 steps are in flight without a register or
+// a barrier; the waves' sums (whole numbers: exact in any order) meet in LDS at the end.
+// Bound by the weights' bytes.
+//
+// v_mfma_i32_16x16x64_i8: lane l holds 16 bytes of row l % 16 from k = 16 (l / 16) on of
+// either operand, and of the result column l % 16, rows 4 (l / 16) .. + 3.  W comes first,
+// so a lane has four neighbouring columns of one row of C.
+#include <algorithm>
+
+#include "fm_i8.hpp"
+#include "fm_i8_tile.hpp"
+
+namespace fm {
+namespace {
+
+constexpr int kFewLds = 152 * 1024;
+
+template <int X8, int C8>
+struct FewShape {
+  static constexpr int LOADS = X8 + C8;                 // 1 KiB each
+  static constexpr int NWV = LOADS <= 9 ? 8 : 4;
+  static constexpr int FIT = kFewLds / (NWV * LOADS * 1024);
+  static constexpr int S = FIT < 4 ? FIT : 4;
+  static constexpr int FM = (X8 + 1) / 2, FN = (C8 + 1) / 2;   // 16 x 16 results
+  static constexpr int RING = NWV * S * LOADS * 1024, SUMS = NWV * FM * FN * 1024;
+  static constexpr int LDS = RING > SUMS ? RING : SUMS;
+  static_assert(S >= 2, "two steps in flight");
+};
+
+// Four results of a row from column n on.
+struct Finish4 {
+  f32x4 scale, bias;
+};
+
+__device__ __forceinline__ Finish4 columns4(const I8Args& a, int64_t n) {
+  Finish4 f = {*reinterpret_cast<const f32x4*>(a.w_scale + n), {0.f, 0.f, 0.f, 0.f}};
+  if (a.bias)
+    f.bias = a.dt == FM_F16 ? load4<F16>(static_cast<const _Float16*>(a.bias) + n)
+                            : load4<BF16>(static_cast<const __bf16*>(a.bias) + n);
+  return f;
+}
+
+__device__ __forceinline__ void store_row4(const I8Args& a, const Finish4& f, i32x4 sum, float sa, int64_t at) {
+  f32x4 v[1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[0][i] = (float)sum[i] * (sa * f.scale[i]) + f.bias[i];
+  activate_all(v, a.act);
+  if (a.c == FM_F32) store4<F32>(reinterpret_cast<float*>(a.C) + at, v[0]);
+  else if (a.c == FM_F16) store4<F16>(reinterpret_cast<_Float16*>(a.C) + at, v[0]);
+  else store4<BF16>(reinterpret_cast<__bf16*>(a.C) + at, v[0]);
+}
+
+template <int X8, int C8>
+__global__ __launch_bounds__((64 * FewShape<X8, C8>::NWV)) void gemm_i8_few(const I8Args a) {
+  using Sh = FewShape<X8, C8>;
+  constexpr int NWV = Sh::NWV, S = Sh::S, LOADS = Sh::LOADS, FM = Sh::FM, FN = Sh::FN;
+  __shared__ __attribute__((aligned(16))) char smem[Sh::LDS];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int M = (int)a.M, K = (int)a.K;
+  const int64_t n0 = (int64_t)blockIdx.x * (8 * C8);
+  const int cols = (int)min((int64_t)(8 * C8), a.N - n0);
+  const int KT = (K + kI8Step - 1) / kI8Step, tail = K % kI8Step;
+  const char* const wt = a.W + n0 * K;
+  char* const ring = smem + w * (S * LOADS * 1024);
+  const uint32_t ring0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)ring);
+
+  // Load d: rows 8 d .. + 7 of x, then of W; rows past the last are read as the last.
+  // Chunk c of row r lies at chunk c ^ swz_a(r).
+  uint32_t off[LOADS];
+#pragma unroll
+  for (int d = 0; d < LOADS; ++d) {
+    const int r = 8 * (d < X8 ? d : d - X8) + (lane >> 3);
+    off[d] = (uint32_t)min(r, (d < X8 ? M : cols) - 1) * (uint32_t)K + (((lane & 7) ^ swz_a(r)) << 4);
+  }
+  auto load = [&](int kt, int slot) {
+    const int64_t k = (int64_t)kt * kI8Step;
+#pragma unroll
+    for (int d = 0; d < LOADS; ++d) {
+      // past K a lane loads its row's first chunk of the step instead
+      const int c = (((lane & 7) ^ swz_a(8 * (d < X8 ? d : d - X8) + (lane >> 3))) << 4);
+      const uint32_t at = kt == KT - 1 && tail && c >= tail ? off[d] - c : off[d];
+      dma16(at, (d < X8 ? a.A : wt) + k, ring0 + (slot * LOADS + d) * 1024);
+    }
+  };
+  // Fragment (16 rows from 16 g on, half h of the step) of x (from = 0) or W (from = X8)
+  // in a slot; an odd number of eights reads its last one twice.
+  auto fragment = [&](const char* s, int from, int eights, int g, int h) {
+    const int r = lane & 15, e = 2 * g + (2 * g + 1 < eights ? r >> 3 : 0);
+    const int row = 8 * e + (r & 7), c = (4 * h + (lane >> 4)) ^ swz_a(row);
+    return *reinterpret_cast<const i32x4*>(s + (from + e) * 1024 + (r & 7) * kI8Step + c * 16);
+  };
+
+  i32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  const int steps = KT > w ? (KT - w + NWV - 1) / NWV : 0;   // this wave's
+  for (int i = 0; i < S && i < steps; ++i) load(w + i * NWV, i);
+  int slot = 0;
+  for (int i = 0; i < steps; ++i) {
+    if (i + S <= steps) wait_vm_mem<(S - 1) * LOADS>();
+    else wait_vm_mem<0>();
+    const int kt = w + i * NWV;
+    const char* s = ring + slot * LOADS * 1024;
+    if (kt == KT - 1 && tail) {
+#pragma unroll
+      for (int d = 0; d < X8; ++d)
+        if (((((lane & 7) ^ swz_a(8 * d + (lane >> 3))) << 4)) >= tail)
+          *reinterpret_cast<u32x4*>(const_cast<char*>(s) + d * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+      wait_lgkm_mem();
+    }
+    i32x4 fx[2][FM], fw[2][FN];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int g = 0; g < FN; ++g) fw[h][g] = fragment(s, X8, C8, g, h);
+#pragma unroll
+      for (int g = 0; g < FM; ++g) fx[h][g] = fragment(s, 0, X8, g, h);
+    }
+    wait_lgkm_mem();   // read before the slot is filled again
+    if (i + S < steps) load(kt + S * NWV, slot);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < FM; ++m)
+#pragma unroll
+        for (int n = 0; n < FN; ++n)
+          acc[m][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h][n], fx[h][m], acc[m][n], 0, 0, 0);
+    slot = slot + 1 == S ? 0 : slot + 1;
+  }
+  __syncthreads();
+  i32x4* const sums = reinterpret_cast<i32x4*>(smem);
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int n = 0; n < FN; ++n) sums[((w * FM + m) * FN + n) * 64 + lane] = acc[m][n];
+  __syncthreads();
+  for (int t = threadIdx.x; t < FM * FN * 64; t += 64 * NWV) {
+    const int l = t & 63, m = (t / 64 / FN) * 16 + (l & 15), n = (t / 64 % FN) * 16 + 4 * (l >> 4);
+    if (m >= M || n >= cols) continue;
+    i32x4 sum = sums[t];
+#pragma unroll
+    for (int o = 1; o < NWV; ++o) sum += sums[o * (FM * FN * 64) + t];
+    store_row4(a, columns4(a, n0 + n), sum, a.a_scale[m], (int64_t)m * a.N + n0 + n);
+  }
+}
+
+template <int X8>
+void launch_columns(const I8Args& a, hipStream_t stream) {
+  const int64_t eights = a.N / 8, per = cdiv(eights, device_cu_count());
+#define FM_FEW(C8)                                                                            \
+  hipLaunchKernelGGL((gemm_i8_few<X8, C8>), dim3((unsigned)cdiv(eights, C8)),                 \
+                     dim3(64 * FewShape<X8, C8>::NWV), 0, stream, a)
+  if (per <= 1) FM_FEW(1);
+  else if (per <= 2) FM_FEW(2);
+  else if (per <= 3) FM_FEW(3);
+  else if (per <= 4) FM_FEW(4);
+  else FM_FEW(6);
+#undef FM_FEW
+}
+
+}  // namespace
+
+void launch_i8_few(const I8Args& a, hipStream_t stream) {
+  if (a.M <= 8) launch_columns<1>(a, stream);
+  else if (a.M <= 16) launch_columns<2>(a, stream);
+  else if (a.M <= 32) launch_columns<4>(a, stream);
+  else if (a.M <= 48) launch_columns<6>(a, stream);
+  else launch_columns<8>(a, stream);
+}
+
+bool i8_few_quantises(int64_t M, int64_t K) { return false; }
+void launch_i8_few_quant(const I8Args& a, hipStream_t stream) {}
+
+}  // namespace fm
