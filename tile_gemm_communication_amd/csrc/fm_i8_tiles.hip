@@ -36,7 +36,9 @@ __device__ __forceinline__ void finish8(const I8Args& a, const Columns& c, const
 template <typename E, typename O, int BM, int BN, int AHEAD>
 __global__ __launch_bounds__(256, 1) void gemm_i8_tiles(const TileArgs a) {
   using Tile = I8Tile<BM, BN, AHEAD>;
-  constexpr int PITCH = Tile::WN * 4 + 16, LPR = Tile::WN / 8;   // staged row, lanes of one
+  // bytes of a staged row, and lanes that take one, eight columns each (rounded up, so that
+  // a lane keeps its columns)
+  constexpr int PITCH = Tile::WN * 4 + 16, LPR = Tile::WN == 96 ? 16 : Tile::WN / 8;
   static_assert(4 * 32 * PITCH + (BM + 2 * BN) * 4 <= Tile::LDS_BYTES && 32 * LPR % 64 == 0, "staging");
   __shared__ __attribute__((aligned(16))) char smem[Tile::LDS_BYTES];
   Tile t(smem, a.K);
@@ -66,6 +68,13 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tiles(const TileArgs a) {
       s_bias[threadIdx.x] = col_bias;
     }
     __syncthreads();
+    const int x = t.lane % LPR * 8, n = t.wn * Tile::WN + x;
+    const bool mine = x < Tile::WN && n < cols;
+    Columns c = {};
+    if (mine) {
+      load8<F32>(s_scale + n, c.scale);
+      load8<F32>(s_bias + n, c.bias);
+    }
 #pragma unroll
     for (int i = 0; i < Tile::FM; ++i) {
       asm volatile("" ::: "memory");   // one block's registers after another's
@@ -80,14 +89,10 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tiles(const TileArgs a) {
       wave_lds_sync();
 #pragma unroll 2
       for (int q = 0; q < 32 * LPR / 64; ++q) {
-        const int k = q * 64 + t.lane, y = k / LPR, x = k % LPR * 8;
-        const int m = t.wm * Tile::WM + 32 * i + y, n = t.wn * Tile::WN + x;
-        if (m < rows && n < cols) {
+        const int y = q * (64 / LPR) + t.lane / LPR, m = t.wm * Tile::WM + 32 * i + y;
+        if (m < rows && mine) {
           const i32x4* p = reinterpret_cast<const i32x4*>(stage + y * PITCH + x * 4);
           const i32x4 sum[2] = {p[0], p[1]};
-          Columns c;
-          load8<F32>(s_scale + n, c.scale);
-          load8<F32>(s_bias + n, c.bias);
           finish8<O>(a, c, sum, s_row[m], (m0 + m) * a.N + n0 + n);
         }
       }
