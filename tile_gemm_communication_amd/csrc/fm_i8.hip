@@ -92,7 +92,7 @@ fm_status_t check_i8(fm_dtype_t dt, fm_dtype_t c, int64_t M, int64_t N, int64_t 
   if ((dt != FM_F16 && dt != FM_BF16) || (c != dt && c != FM_F32)) return FM_ERR_UNSUPPORTED;
   if (M < 0 || N < 0 || K < 0 || N % 8 || K % 16) return FM_ERR_INVALID_ARG;
   if ((int)act < FM_ACT_NONE || (int)act > FM_ACT_SILU) return FM_ERR_INVALID_ARG;
-  if (M >= kI8MaxDim || N >= kI8MaxDim || K > kI8MaxK) return FM_ERR_UNSUPPORTED;
+  if (M >= kI8MaxDim || N >= kI8MaxDim || M * N >= (1ll << 42) || K > kI8MaxK) return FM_ERR_UNSUPPORTED;
   return FM_OK;
 }
 

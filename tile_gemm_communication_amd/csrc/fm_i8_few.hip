@@ -20,17 +20,28 @@ namespace {
 
 constexpr int kFewLds = 152 * 1024;
 
-template <int X8, int C8>
+// What a block quantises for itself: at most 32 pieces of 512 values (four a wave; 17 KiB
+// of codes), in the shadow of the first weights' loads.  1 x 12288 x 6144: 14.7 us, with a
+// launch of its own before it 17.6; of 96 pieces (8 x 6144) it would take 23, against 15.9.
+constexpr int kQuantPiece = 512, kQuantHeld = 4, kQuantMost = 8 * kQuantHeld;
+constexpr int kFewQuantRows = 8, kFewCodes = 17 * 1024;
+
+// X8, C8: eights of x's rows and of columns.  QUANT: the block quantises 16-bit rows first
+// and keeps the codes; else codes are streamed beside the weights.
+template <int X8, int C8, bool QUANT>
 struct FewShape {
-  static constexpr int LOADS = X8 + C8;                 // 1 KiB each
+  static constexpr int X_LOADS = QUANT ? 0 : X8, LOADS = X_LOADS + C8;   // 1 KiB each
   static constexpr int NWV = LOADS <= 9 ? 8 : 4;
-  static constexpr int FIT = kFewLds / (NWV * LOADS * 1024);
+  static constexpr int X_BYTES = QUANT ? kFewCodes : 0;
+  static constexpr int FIT = (kFewLds - X_BYTES) / (NWV * LOADS * 1024);
   static constexpr int S = FIT < 4 ? FIT : 4;
   static constexpr int FM = (X8 + 1) / 2, FN = (C8 + 1) / 2;   // 16 x 16 results
   static constexpr int RING = NWV * S * LOADS * 1024, SUMS = NWV * FM * FN * 1024;
   static constexpr int LDS = RING > SUMS ? RING : SUMS;
   static_assert(S >= 2, "two steps in flight");
 };
+
+__host__ __device__ inline int code_pitch(int K) { return (K + 255) / 256 * 256 + 64; }
 
 // Four results of a row from column n on.
 struct Finish4 {
@@ -55,11 +66,61 @@ __device__ __forceinline__ void store_row4(const I8Args& a, const Finish4& f, i3
   else store4<BF16>(reinterpret_cast<__bf16*>(a.C) + at, v[0]);
 }
 
-template <int X8, int C8>
-__global__ __launch_bounds__((64 * FewShape<X8, C8>::NWV)) void gemm_i8_few(const I8Args a) {
-  using Sh = FewShape<X8, C8>;
-  constexpr int NWV = Sh::NWV, S = Sh::S, LOADS = Sh::LOADS, FM = Sh::FM, FN = Sh::FN;
-  __shared__ __attribute__((aligned(16))) char smem[Sh::LDS];
+// The rows of x as codes at `codes`, zeros from K to the
+// end of the last step, and their scales; the loads first, so that the weights' can
+// follow them before `start()` returns.  Ends behind a barrier.
+template <class F>
+__device__ __forceinline__ void quantise_rows(const I8Args& a, int w, int lane, int KT, char* codes,
+                                              uint32_t* tops, float* scales, F&& start) {
+  const int K = (int)a.K, M = (int)a.M, pieces = (K + kQuantPiece - 1) / kQuantPiece;
+  const int total = M * pieces, pitch = code_pitch(K);
+  u32x4 v[kQuantHeld];
+#pragma unroll
+  for (int i = 0; i < kQuantHeld; ++i) {
+    const int g = i * 8 + w, row = g / pieces, e = (g - row * pieces) * kQuantPiece + lane * 8;
+    v[i] = u32x4{0, 0, 0, 0};
+    if (g < total && e < K) v[i] = *reinterpret_cast<const u32x4*>(a.A + ((int64_t)row * K + e) * 2);
+  }
+  start();
+  auto widened = [&](const u32x4& r, int h) {
+    const u32x2 p = {r[2 * h], r[2 * h + 1]};
+    return a.dt == FM_F16 ? widen<F16>(__builtin_bit_cast(f16x4, p)) : widen<BF16>(__builtin_bit_cast(bf16x4, p));
+  };
+#pragma unroll
+  for (int i = 0; i < kQuantHeld; ++i) {
+    const int g = i * 8 + w;
+    if (g >= total) break;
+    uint32_t top = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 x = widened(v[i], h);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = max(top, magnitude(x[k]));
+    }
+    top = group_umax<64>(top);
+    if (lane == 0) tops[g] = top;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQuantHeld; ++i) {
+    const int g = i * 8 + w, row = g / pieces, e = (g - row * pieces) * kQuantPiece + lane * 8;
+    if (g >= total) break;
+    const RowQuant r = row_quant(group_umax<64>(lane < pieces ? tops[row * pieces + lane] : 0u));
+    if (e == 0) scales[row] = r.scale;
+    if (e < KT * kI8Step)
+      *reinterpret_cast<u32x2*>(codes + row * pitch + e) = u32x2{quant4(widened(v[i], 0), r), quant4(widened(v[i], 1), r)};
+  }
+  __syncthreads();
+}
+
+template <int X8, int C8, bool QUANT>
+__global__ __launch_bounds__((64 * FewShape<X8, C8, QUANT>::NWV)) void gemm_i8_few(const I8Args a) {
+  using Sh = FewShape<X8, C8, QUANT>;
+  constexpr int NWV = Sh::NWV, S = Sh::S, LOADS = Sh::LOADS, XL = Sh::X_LOADS, FM = Sh::FM, FN = Sh::FN;
+  static_assert(!QUANT || NWV == 8, "pieces go to eight waves");
+  __shared__ __attribute__((aligned(16))) char smem[Sh::LDS + Sh::X_BYTES];
+  __shared__ uint32_t s_tops[QUANT ? kQuantMost : 1];
+  __shared__ float s_scale[kFewQuantRows];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int M = (int)a.M, K = (int)a.K;
   const int64_t n0 = (int64_t)blockIdx.x * (8 * C8);
@@ -67,6 +128,7 @@ __global__ __launch_bounds__((64 * FewShape<X8, C8>::NWV)) void gemm_i8_few(cons
   const int KT = (K + kI8Step - 1) / kI8Step, tail = K % kI8Step;
   const char* const wt = a.W + n0 * K;
   char* const ring = smem + w * (S * LOADS * 1024);
+  char* const codes = smem + Sh::LDS;
   const uint32_t ring0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)ring);
 
   // Load d: rows 8 d .. + 7 of x, then of W; rows past the last are read as the last.
@@ -74,20 +136,20 @@ __global__ __launch_bounds__((64 * FewShape<X8, C8>::NWV)) void gemm_i8_few(cons
   uint32_t off[LOADS];
 #pragma unroll
   for (int d = 0; d < LOADS; ++d) {
-    const int r = 8 * (d < X8 ? d : d - X8) + (lane >> 3);
-    off[d] = (uint32_t)min(r, (d < X8 ? M : cols) - 1) * (uint32_t)K + (((lane & 7) ^ swz_a(r)) << 4);
+    const int r = 8 * (d < XL ? d : d - XL) + (lane >> 3);
+    off[d] = (uint32_t)min(r, (d < XL ? M : cols) - 1) * (uint32_t)K + (((lane & 7) ^ swz_a(r)) << 4);
   }
   auto load = [&](int kt, int slot) {
     const int64_t k = (int64_t)kt * kI8Step;
 #pragma unroll
     for (int d = 0; d < LOADS; ++d) {
       // past K a lane loads its row's first chunk of the step instead
-      const int c = (((lane & 7) ^ swz_a(8 * (d < X8 ? d : d - X8) + (lane >> 3))) << 4);
+      const int c = (((lane & 7) ^ swz_a(8 * (d < XL ? d : d - XL) + (lane >> 3))) << 4);
       const uint32_t at = kt == KT - 1 && tail && c >= tail ? off[d] - c : off[d];
-      dma16(at, (d < X8 ? a.A : wt) + k, ring0 + (slot * LOADS + d) * 1024);
+      dma16(at, (d < XL ? a.A : wt) + k, ring0 + (slot * LOADS + d) * 1024);
     }
   };
-  // Fragment (16 rows from 16 g on, half h of the step) of x (from = 0) or W (from = X8)
+  // Fragment (16 rows from 16 g on, half h of the step) of x (from = 0) or W (from = XL)
   // in a slot; an odd number of eights reads its last one twice.
   auto fragment = [&](const char* s, int from, int eights, int g, int h) {
     const int r = lane & 15, e = 2 * g + (2 * g + 1 < eights ? r >> 3 : 0);
@@ -101,16 +163,20 @@ __global__ __launch_bounds__((64 * FewShape<X8, C8>::NWV)) void gemm_i8_few(cons
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
   const int steps = KT > w ? (KT - w + NWV - 1) / NWV : 0;   // this wave's
-  for (int i = 0; i < S && i < steps; ++i) load(w + i * NWV, i);
+  auto start = [&] {
+    for (int i = 0; i < S && i < steps; ++i) load(w + i * NWV, i);
+  };
+  if constexpr (QUANT) quantise_rows(a, w, lane, KT, codes, s_tops, s_scale, start);
+  else start();
   int slot = 0;
   for (int i = 0; i < steps; ++i) {
     if (i + S <= steps) wait_vm_mem<(S - 1) * LOADS>();
     else wait_vm_mem<0>();
     const int kt = w + i * NWV;
     const char* s = ring + slot * LOADS * 1024;
-    if (kt == KT - 1 && tail) {
+    if (!QUANT && kt == KT - 1 && tail) {   // x counts as 0 past K
 #pragma unroll
-      for (int d = 0; d < X8; ++d)
+      for (int d = 0; d < XL; ++d)
         if (((((lane & 7) ^ swz_a(8 * d + (lane >> 3))) << 4)) >= tail)
           *reinterpret_cast<u32x4*>(const_cast<char*>(s) + d * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
       wait_lgkm_mem();
@@ -119,9 +185,14 @@ __global__ __launch_bounds__((64 * FewShape<X8, C8>::NWV)) void gemm_i8_few(cons
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int g = 0; g < FN; ++g) fw[h][g] = fragment(s, X8, C8, g, h);
+      for (int g = 0; g < FN; ++g) fw[h][g] = fragment(s, XL, C8, g, h);
 #pragma unroll
-      for (int g = 0; g < FM; ++g) fx[h][g] = fragment(s, 0, X8, g, h);
+      for (int g = 0; g < FM; ++g) {
+        if constexpr (QUANT)
+          fx[h][g] = *reinterpret_cast<const i32x4*>(codes + min(lane & 15, M - 1) * code_pitch(K) + kt * kI8Step +
+                                                     (4 * h + (lane >> 4)) * 16);
+        else fx[h][g] = fragment(s, 0, X8, g, h);
+      }
     }
     wait_lgkm_mem();   // read before the slot is filled again
     if (i + S < steps) load(kt + S * NWV, slot);
@@ -147,16 +218,17 @@ __global__ __launch_bounds__((64 * FewShape<X8, C8>::NWV)) void gemm_i8_few(cons
     i32x4 sum = sums[t];
 #pragma unroll
     for (int o = 1; o < NWV; ++o) sum += sums[o * (FM * FN * 64) + t];
-    store_row4(a, columns4(a, n0 + n), sum, a.a_scale[m], (int64_t)m * a.N + n0 + n);
+    store_row4(a, columns4(a, n0 + n), sum, QUANT ? s_scale[m % kFewQuantRows] : a.a_scale[m],
+               (int64_t)m * a.N + n0 + n);
   }
 }
 
-template <int X8>
+template <int X8, bool QUANT>
 void launch_columns(const I8Args& a, hipStream_t stream) {
   const int64_t eights = a.N / 8, per = cdiv(eights, device_cu_count());
 #define FM_FEW(C8)                                                                            \
-  hipLaunchKernelGGL((gemm_i8_few<X8, C8>), dim3((unsigned)cdiv(eights, C8)),                 \
-                     dim3(64 * FewShape<X8, C8>::NWV), 0, stream, a)
+  hipLaunchKernelGGL((gemm_i8_few<X8, C8, QUANT>), dim3((unsigned)cdiv(eights, C8)),              \
+                     dim3(64 * FewShape<X8, C8, QUANT>::NWV), 0, stream, a)
   if (per <= 1) FM_FEW(1);
   else if (per <= 2) FM_FEW(2);
   else if (per <= 3) FM_FEW(3);
@@ -168,14 +240,18 @@ void launch_columns(const I8Args& a, hipStream_t stream) {
 }  // namespace
 
 void launch_i8_few(const I8Args& a, hipStream_t stream) {
-  if (a.M <= 8) launch_columns<1>(a, stream);
-  else if (a.M <= 16) launch_columns<2>(a, stream);
-  else if (a.M <= 32) launch_columns<4>(a, stream);
-  else if (a.M <= 48) launch_columns<6>(a, stream);
-  else launch_columns<8>(a, stream);
+  if (a.M <= 8) launch_columns<1, false>(a, stream);
+  else if (a.M <= 16) launch_columns<2, false>(a, stream);
+  else if (a.M <= 32) launch_columns<4, false>(a, stream);
+  else if (a.M <= 48) launch_columns<6, false>(a, stream);
+  else launch_columns<8, false>(a, stream);
 }
 
-bool i8_few_quantises(int64_t M, int64_t K) { return false; }
-void launch_i8_few_quant(const I8Args& a, hipStream_t stream) {}
+bool i8_few_quantises(int64_t M, int64_t K) {
+  return M <= kFewQuantRows && K > 0 && M * cdiv(K, kQuantPiece) <= kQuantMost &&
+         M * code_pitch((int)K) <= kFewCodes;
+}
+
+void launch_i8_few_quant(const I8Args& a, hipStream_t stream) { launch_columns<1, true>(a, stream); }
 
 }  // namespace fm

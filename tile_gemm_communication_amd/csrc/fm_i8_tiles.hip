@@ -1,6 +1,5 @@
 // fm_i8_tiles.hip -- 8-bit products of many rows.
 #include <algorithm>
-#include <cstdlib>
 
 #include "fm_i8.hpp"
 #include "fm_i8_tile.hpp"
@@ -102,45 +101,73 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tiles(const TileArgs a) {
   }
 }
 
+// The tile of a product by what its rounds take: a K step of one block on a compute unit
+// alone, of each of two there, and a tile's fixed part (us).  Fitted to 180 products of
+// 65..8192 rows, 1024..12288 columns and as much k (the choice is 0.5% slower than the best
+// of the seven on average; 64 x 64 tiles for all would be 26%, 256 x 256 for all 120%).  The
+// small tiles are bound by what a compute unit gets from L2 (16 KiB a step in 0.2 us), the
+// large ones by the matrix cores under the power limit.
+struct TileChoice {
+  int bm, bn, resident;
+  double alone, shared, fixed;
+};
+constexpr TileChoice kTileChoices[] = {
+    {64, 64, 2, 0.195, 0.397, 1.4},   {64, 128, 2, 0.267, 0.639, 2.1}, {128, 128, 1, 0.403, 0, 3.6},
+    {128, 192, 1, 0.499, 0, 6.0},     {256, 128, 1, 0.631, 0, 5.7},    {256, 192, 1, 0.808, 0, 9.6},
+    {256, 256, 1, 1.012, 0, 9.8},
+};
+
+int choose_tile(int64_t M, int64_t N, int64_t K, int cus) {
+  const double steps = (double)cdiv(K, kI8Step);
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < (int)(sizeof(kTileChoices) / sizeof(kTileChoices[0])); ++i) {
+    const TileChoice& c = kTileChoices[i];
+    const int64_t each = cdiv(cdiv(M, c.bm) * cdiv(N, c.bn), cus);
+    const double one = steps * c.alone + c.fixed, two = steps * c.shared + c.fixed;
+    const double time = c.resident == 1 ? each * one : each / 2 * two + each % 2 * one;
+    if (i == 0 || time < least) {
+      best = i;
+      least = time;
+    }
+  }
+  return best;
+}
+
 template <typename E, typename O, int BM, int BN, int AHEAD>
-void launch_grid(const I8Args& g, hipStream_t stream) {
+void launch_grid(const I8Args& g, int resident, hipStream_t stream) {
   TileArgs a = {g};
   a.tiles_m = (int)cdiv(a.M, BM);
   a.tiles_n = (int)cdiv(a.N, BN);
   a.group_m = std::min(8, a.tiles_m);
-  const int64_t total = (int64_t)a.tiles_m * a.tiles_n;
-  hipLaunchKernelGGL((gemm_i8_tiles<E, O, BM, BN, AHEAD>), dim3((unsigned)std::min<int64_t>(total, device_cu_count() * std::min<int>(3, 160 * 1024 / I8Tile<BM, BN, AHEAD>::LDS_BYTES))),
-                     dim3(256), 0, stream, a);
+  const int64_t total = (int64_t)a.tiles_m * a.tiles_n, most = (int64_t)device_cu_count() * resident;
+  hipLaunchKernelGGL((gemm_i8_tiles<E, O, BM, BN, AHEAD>), dim3((unsigned)std::min(total, most)), dim3(256), 0,
+                     stream, a);
 }
 
 template <typename E, typename O>
-void launch_gemm(const I8Args& a, hipStream_t stream) {
-  const char* v = std::getenv("FM_I8");
-  const int k = v ? std::atoi(v) : 0;
-  if (k == 1) return launch_grid<E, O, 256, 256, 2>(a, stream);
-  if (k == 2) return launch_grid<E, O, 256, 192, 2>(a, stream);
-  if (k == 3) return launch_grid<E, O, 256, 128, 2>(a, stream);
-  if (k == 4) return launch_grid<E, O, 192, 192, 2>(a, stream);
-  if (k == 5) return launch_grid<E, O, 128, 128, 2>(a, stream);
-  if (k == 6) return launch_grid<E, O, 128, 64, 3>(a, stream);
-  if (k == 7) return launch_grid<E, O, 64, 64, 2>(a, stream);
-  if (k == 8) return launch_grid<E, O, 192, 256, 2>(a, stream);
-  if (k == 9) return launch_grid<E, O, 128, 192, 3>(a, stream);
-  if (k == 10) return launch_grid<E, O, 128, 128, 4>(a, stream);
-  if (k == 11) return launch_grid<E, O, 64, 64, 4>(a, stream);
-  if (k == 12) return launch_grid<E, O, 64, 128, 3>(a, stream);
-  return launch_grid<E, O, 64, 64, 2>(a, stream);
+void launch_types(const I8Args& a, hipStream_t stream) {
+  const int i = choose_tile(a.M, a.N, a.K, device_cu_count()), r = kTileChoices[i].resident;
+  switch (i) {
+    case 0: return launch_grid<E, O, 64, 64, 4>(a, r, stream);
+    case 1: return launch_grid<E, O, 64, 128, 3>(a, r, stream);
+    case 2: return launch_grid<E, O, 128, 128, 4>(a, r, stream);
+    case 3: return launch_grid<E, O, 128, 192, 3>(a, r, stream);
+    case 4: return launch_grid<E, O, 256, 128, 2>(a, r, stream);
+    case 5: return launch_grid<E, O, 256, 192, 2>(a, r, stream);
+    default: return launch_grid<E, O, 256, 256, 2>(a, r, stream);
+  }
 }
 
 }  // namespace
 
 void launch_i8_tiles(const I8Args& a, hipStream_t stream) {
   if (a.dt == FM_F16) {
-    if (a.c == FM_F32) launch_gemm<F16, F32>(a, stream);
-    else launch_gemm<F16, F16>(a, stream);
+    if (a.c == FM_F32) launch_types<F16, F32>(a, stream);
+    else launch_types<F16, F16>(a, stream);
   } else {
-    if (a.c == FM_F32) launch_gemm<BF16, F32>(a, stream);
-    else launch_gemm<BF16, BF16>(a, stream);
+    if (a.c == FM_F32) launch_types<BF16, F32>(a, stream);
+    else launch_types<BF16, BF16>(a, stream);
   }
 }
 
