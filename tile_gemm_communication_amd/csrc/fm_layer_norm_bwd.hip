@@ -2,7 +2,7 @@
 //
 // One pass over the rows gives d_resid and d_block and, in registers, each lane's
 // share of the three column sums (bias and both norm weights).  A block holds RW rows
-// of TH lanes at a time, each row lane walking its own contiguous rows; at its end
+// of TH lanes at a time, the row lanes of all blocks taking rows in turn; at its end
 // the block writes one partial row a sum, and a second launch joins the partial
 // rows in order (no atomics: the same bits on every call).  Bound by the bytes of the
 // [M, N] arrays.
@@ -40,16 +40,19 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
   constexpr int RW = ln_rows<TH>();
   constexpr f32x4 kZero = {0.f, 0.f, 0.f, 0.f};
   __shared__ f32x2 s_red[2][RW][TH / 64];
-  // 1024 lanes have 128 registers each.  The longest rows keep the sums of both norm
-  // weights in LDS, each lane's in places of its own, and read d_out behind the barrier.
-  constexpr bool kRoom = TH * CH < 2048;
+  // Rows from 8200 elements on keep their sums in LDS, each lane's in places of its own; the
+  // registers hold the next row instead, which is on its way while this one is worked on.
+  // 1024 lanes have 128 registers each: the longest rows (from 12296 on) do without that,
+  // and read d_out behind the barrier; of their sums LDS holds two.
+  constexpr bool kRoom = CH == 1, kAhead = TH * CH < 2048, kBiasRoom = kRoom || !kAhead;
   // joins the row lanes' sums, or holds the lanes' own
-  __shared__ f32x4 s_acc[!kRoom ? 2 * TH * CH * 2 : RW > 1 ? RW * TH * CH * 2 : 1];
+  __shared__ f32x4 s_acc[!kRoom ? (kBiasRoom ? 2 : 3) * TH * CH * 2 : RW > 1 ? RW * TH * CH * 2 : 1];
   const int t = threadIdx.x % TH, N = a.N;
   const int rw = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TH);   // the same in a wave
   const int64_t parts = (int64_t)gridDim.x * RW, part = (int64_t)blockIdx.x * RW + rw;
-  const int64_t first = part * a.M / parts, last = (part + 1) * a.M / parts;
-  // every row lane takes part in the barriers of the longest: M / parts rows or one more
+  // row lanes take rows in turn, so that the rows in work lie side by side (each walking its
+  // own stretch, equally far apart in memory: 16384 x 4096 145 us, so 131); all take part in the
+  // barriers of the longest
   const int64_t count = (a.M + parts - 1) / parts;
   const float invN = 1.f / (float)N;
   const bool has_d = a.d_block || a.part_bias;
@@ -63,32 +66,47 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
     for (int h = 0; h < 2; ++h) {
       acc_w[c][h] = acc_b[c][h] = acc_bias[c][h] = kZero;
       if (!kRoom) s_acc[(c * 2 + h) * TH + t] = s_acc[((CH + c) * 2 + h) * TH + t] = kZero;
+      if (!kBiasRoom) s_acc[((2 * CH + c) * 2 + h) * TH + t] = kZero;
     }
     w[c] = {};
     if (a.w && (c * TH + t) * 8 < N) w[c] = raw8<E>(a.w, (c * TH + t) * 8);
   }
 
-  for (int64_t i = 0; i < count; ++i) {
-    const int64_t row = first + i;
-    const bool live = row < last;
-    const int64_t at = row * N;
-    // rows are held as they came and widened in both passes: half the registers
+  // rows are held as they came and widened in both passes: half the registers
+  struct Row {
     Raw8<E> d_y[CH];
     Raw8<S> out[CH], d_out[CH];
-    const float r = live && a.w ? a.rstd[row] : 0.f, mean = live && a.w ? a.mean[row] : 0.f;
+    float mean, rstd;
+  };
+  auto load = [&](int64_t i) {
+    Row v = {};
+    const int64_t row = part + i * parts, at = row * N;
+    const bool live = row < a.M;
+    if (live && a.w) {
+      v.mean = a.mean[row];
+      v.rstd = a.rstd[row];
+    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int e = (c * TH + t) * 8;
-      const bool in = live && e < N;
-      d_y[c] = {};
-      out[c] = {};
-      d_out[c] = {};
-      if (in && a.w) {
-        d_y[c] = raw8<E>(a.d_y, at + e);
-        out[c] = raw8<S>(a.out, at + e);
+      if (!live || e >= N) continue;
+      if (a.w) {
+        v.d_y[c] = raw8<E>(a.d_y, at + e);
+        v.out[c] = raw8<S>(a.out, at + e);
       }
-      if (kRoom && in && a.d_out) d_out[c] = raw8<S>(a.d_out, at + e);
+      if (kAhead && a.d_out) v.d_out[c] = raw8<S>(a.d_out, at + e);
     }
+    return v;
+  };
+
+  Row next = load(0);
+  for (int64_t i = 0; i < count; ++i) {
+    const int64_t row = part + i * parts;
+    const bool live = row < a.M;
+    const int64_t at = row * N;
+    Row v = next;
+    if (kAhead) next = load(i + 1);
+    const float r = v.rstd, mean = v.mean;
     // dz = r * (t - mean(t) - hat * mean(t hat)) + d_out, t = d_y w
     float s1 = 0.f, s2 = 0.f;
     if (a.w) {
@@ -97,8 +115,8 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
         if ((c * TH + t) * 8 >= N) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const f32x4 dy = half8<E>(d_y[c], h), hat = (half8<S>(out[c], h) - mean) * r;
-          const f32x4 v = dy * half8<E>(w[c], h);
+          const f32x4 dy = half8<E>(v.d_y[c], h), hat = (half8<S>(v.out[c], h) - mean) * r;
+          const f32x4 q = dy * half8<E>(w[c], h);
           if (kRoom) {
             acc_b[c][h] += dy;
             acc_w[c][h] += dy * hat;
@@ -106,8 +124,8 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
             s_acc[(c * 2 + h) * TH + t] += dy;
             s_acc[((CH + c) * 2 + h) * TH + t] += dy * hat;
           }
-          s1 += (v[0] + v[1]) + (v[2] + v[3]);
-          s2 += dot4(v, hat);
+          s1 += (q[0] + q[1]) + (q[2] + q[3]);
+          s2 += dot4(q, hat);
         }
       }
       s1 = group_sum<64>(s1);
@@ -131,16 +149,16 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
     for (int c = 0; c < CH; ++c) {
       const int e = (c * TH + t) * 8;
       if (!live || e >= N) continue;
-      if (!kRoom && a.d_out) d_out[c] = raw8<S>(a.d_out, at + e);
-      hold(d_y[c]);
-      hold(out[c]);
+      if (!kAhead && a.d_out) v.d_out[c] = raw8<S>(a.d_out, at + e);
+      hold(v.d_y[c]);
+      hold(v.out[c]);
       f32x4 dz[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        dz[h] = half8<S>(d_out[c], h);
+        dz[h] = half8<S>(v.d_out[c], h);
         if (a.w) {
-          const f32x4 hat = (half8<S>(out[c], h) - mean) * r;
-          dz[h] += (half8<E>(d_y[c], h) * half8<E>(w[c], h) - s1 - hat * s2) * r;
+          const f32x4 hat = (half8<S>(v.out[c], h) - mean) * r;
+          dz[h] += (half8<E>(v.d_y[c], h) * half8<E>(w[c], h) - s1 - hat * s2) * r;
         }
       }
       if (a.d_resid) store8<S>(static_cast<typename Elem<S>::type*>(a.d_resid) + at + e, dz);
@@ -151,10 +169,14 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
           dz[1] = drop4(dz[1], k[2], k[3], a.d);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) acc_bias[c][h] += dz[h];
+        for (int h = 0; h < 2; ++h) {
+          if (kBiasRoom) acc_bias[c][h] += dz[h];
+          else s_acc[((2 * CH + c) * 2 + h) * TH + t] += dz[h];
+        }
         if (a.d_block) store8<B>(static_cast<typename Elem<B>::type*>(a.d_block) + at + e, dz);
       }
     }
+    if (!kAhead) next = load(i + 1);
   }
   auto flush = [&](f32x4 (&acc)[CH][2], float* to) {
     if (!to) return;
@@ -188,6 +210,7 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
       for (int h = 0; h < 2; ++h) {
         acc_b[c][h] = s_acc[(c * 2 + h) * TH + t];
         acc_w[c][h] = s_acc[((CH + c) * 2 + h) * TH + t];
+        if (!kBiasRoom) acc_bias[c][h] = s_acc[((2 * CH + c) * 2 + h) * TH + t];
       }
   }
   flush(acc_bias, a.part_bias);
