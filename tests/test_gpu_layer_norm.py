@@ -83,6 +83,9 @@ CASES = [  # M, N, dt, stream, block ("none": no block), bias, norm, p
     (2, 72, "bf16", "bf16", "bf16", 0, 1, 1.0),
     (50, 640, "bf16", "bf16", "none", 0, 1, 0.0),
     (50, 136, "fp16", "fp32", "fp32", 1, 0, 0.0),
+    (1031, 256, "bf16", "bf16", "fp32", 1, 1, 0.1),
+    (70, 128, "fp16", "fp32", "fp16", 1, 1, 0.1),
+    (33, 120, "bf16", "bf16", "bf16", 1, 1, 0.1),
 ]
 
 

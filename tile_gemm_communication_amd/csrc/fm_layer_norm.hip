@@ -26,10 +26,10 @@ struct LnArgs {
 template <typename E, typename S, typename B, int TH, int CH>
 __global__ __launch_bounds__(TH < 256 ? 256 : TH) void layer_norm_fwd(const LnArgs a) {
   constexpr int RW = TH < 256 ? 256 / TH : 1;
-  __shared__ float s_red[2][RW][TH / 64];
-  __shared__ uint32_t s_top[RW][TH / 64];
+  __shared__ float s_red[2][RW][(TH + 63) / 64];
+  __shared__ uint32_t s_top[RW][(TH + 63) / 64];
   const int t = threadIdx.x % TH, N = a.N;
-  const int rw = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TH);   // the same in a wave
+  const int rw = row_lane<TH>();
   const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RW + rw;
   if (TH == 64 && row >= a.M) return;   // whole waves, and no barrier follows
   const bool live = row < a.M;
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void layer_norm_fwd(const LnAr
       store8<S>(static_cast<typename Elem<S>::type*>(a.out) + at + e, z[c]);
   }
   if (!a.w) return;
-  const float mean = row_sum<TH>(s, s_red[0][rw]) * invN;
+  const float mean = ln_sum<TH>(s, s_red[0][rw]) * invN;
   float ss = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void layer_norm_fwd(const LnAr
       }
     }
   }
-  const float r = rstd_of(row_sum<TH>(ss, s_red[1][rw]) * invN, a.eps);
+  const float r = rstd_of(ln_sum<TH>(ss, s_red[1][rw]) * invN, a.eps);
   if (live && t == 0) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = r;

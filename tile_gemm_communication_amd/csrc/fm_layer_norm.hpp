@@ -14,7 +14,9 @@ fm_status_t check_layer_norm(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t blo
 // 768 lanes fit 12288 elements exactly.
 #define FM_LN_SIZES(N, F)            \
   do {                               \
-    if ((N) <= 512) F(64, 1);        \
+    if ((N) <= 128) F(16, 1);        \
+    else if ((N) <= 256) F(32, 1);   \
+    else if ((N) <= 512) F(64, 1);   \
     else if ((N) <= 1024) F(128, 1); \
     else if ((N) <= 2048) F(256, 1); \
     else if ((N) <= 4096) F(512, 1); \
@@ -22,6 +24,20 @@ fm_status_t check_layer_norm(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t blo
     else if ((N) <= 12288) F(768, 2);\
     else F(1024, 2);                 \
   } while (0)
+
+// The row lane of a thread, where it is one for a whole wave in a scalar register.
+template <int TH>
+__device__ __forceinline__ int row_lane() {
+  const int rw = (int)threadIdx.x / TH;
+  return TH < 64 ? rw : __builtin_amdgcn_readfirstlane(rw);
+}
+
+// row_sum, also of rows that share a wave.
+template <int TH>
+__device__ __forceinline__ float ln_sum(float x, float* slots) {
+  if constexpr (TH < 64) return group_sum<TH>(x);
+  else return row_sum<TH>(x, slots);
+}
 
 // Rows in 8 bits: scale = max|x| / 127, q = x * 127 / max|x| rounded to nearest
 // even.  A row whose largest magnitude is below 2^-100 is held as zeros with scale
@@ -70,7 +86,7 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t x) {
 
 template <int TH>
 __device__ __forceinline__ uint32_t row_umax(uint32_t x, uint32_t* slots) {
-  x = group_umax<64>(x);
+  x = group_umax<TH < 64 ? TH : 64>(x);
   if constexpr (TH > 64) {
     const int t = threadIdx.x % TH;
     if (t % 64 == 0) slots[t / 64] = x;

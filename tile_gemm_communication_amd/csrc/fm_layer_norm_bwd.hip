@@ -39,7 +39,7 @@ template <typename E, typename S, typename B, int TH, int CH>
 __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const LnBwdArgs a) {
   constexpr int RW = ln_rows<TH>();
   constexpr f32x4 kZero = {0.f, 0.f, 0.f, 0.f};
-  __shared__ f32x2 s_red[2][RW][TH / 64];
+  __shared__ f32x2 s_red[2][RW][(TH + 63) / 64];
   // Rows from 8200 elements on keep their sums in LDS, each lane's in places of its own; the
   // registers hold the next row instead, which is on its way while this one is worked on.
   // 1024 lanes have 128 registers each: the longest rows (from 12296 on) do without that,
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
   // joins the row lanes' sums, or holds the lanes' own
   __shared__ f32x4 s_acc[!kRoom ? (kBiasRoom ? 2 : 3) * TH * CH * 2 : RW > 1 ? RW * TH * CH * 2 : 1];
   const int t = threadIdx.x % TH, N = a.N;
-  const int rw = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TH);   // the same in a wave
+  const int rw = row_lane<TH>();
   const int64_t parts = (int64_t)gridDim.x * RW, part = (int64_t)blockIdx.x * RW + rw;
   // row lanes take rows in turn, so that the rows in work lie side by side (each walking its
   // own stretch, equally far apart in memory: 16384 x 4096 145 us, so 131); all take part in the
@@ -128,8 +128,8 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
           s2 += dot4(q, hat);
         }
       }
-      s1 = group_sum<64>(s1);
-      s2 = group_sum<64>(s2);
+      s1 = group_sum<TH < 64 ? TH : 64>(s1);
+      s2 = group_sum<TH < 64 ? TH : 64>(s2);
       if constexpr (TH > 64) {
         // the other slot is written before the next barrier: one barrier a row
         f32x2* slots = s_red[i & 1][rw];
@@ -192,6 +192,7 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
         for (int c = 0; c < CH; ++c)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
+#pragma unroll 4
             for (int o = 1; o < RW; ++o) acc[c][h] += s_acc[((o * CH + c) * 2 + h) * TH + t];
       }
     }
