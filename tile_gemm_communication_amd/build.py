@@ -131,7 +131,7 @@ def build(verbose: bool = True) -> str:
             _link_module(module.result())
         else:
             print("torch is not installed: _fluxmi.so, which the Python binding of the router, "
-                  "norms and 4-bit products needs, is not built", file=sys.stderr)
+                  "norms, dropout, 4-bit and 8-bit products needs, is not built", file=sys.stderr)
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB

@@ -10,8 +10,11 @@ namespace fm {
 fm_status_t check_layer_norm(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t block_dt, int64_t M,
                              int64_t N, float p, const uint64_t* rng, int64_t row_begin);
 
-// Lanes and chunks of eight elements that hold a row of N: F(lanes, chunks).
-// 768 lanes fit 12288 elements exactly.
+// Lanes and chunks of eight elements that hold a row of N: F(lanes, chunks).  Forward,
+// us: 65536 x 256 with 32 lanes 29, 64 43; 16384 x 4096 with 512 lanes 120, 256 twice 120
+// (509 rows: 5.1, 5.9); 8192 x 8192 fp32 with 1024 169, 512 twice 172; 4088 x 12288 with 768
+// twice, which fit exactly, 132, 512 three times 137; 4088 x 16384 bf16 with 1024 twice 104,
+// 512 four times 131.
 #define FM_LN_SIZES(N, F)            \
   do {                               \
     if ((N) <= 128) F(16, 1);        \
