@@ -730,9 +730,11 @@ fm_status_t fm_moe_gemm_scatter_w4(fm_dtype_t dt, int64_t T, int64_t hidden, int
  *   p          share of dropped elements, 0..1; 0 copies, 1 clears.
  *   rng        device uint64 [2]: seed and offset; read when the kernel runs, so a
  *              captured graph draws anew if the program advances rng[1] between
- *              replays.  NULL only with p = 0.
+ *              replays.  8-byte aligned; NULL only with p = 0.
  *   draw       added to the offset (both wrap round): one number for each place of a
- *              program that draws, the same in forward and backward.
+ *              program that draws, the same in forward and backward.  Two draws with one
+ *              sum share their mask: a program whose places have the numbers 0 .. n - 1
+ *              advances rng[1] by n from step to step.
  *   row_begin, col_begin  >= 0; col_begin a multiple of 8; row_begin + M at most
  *              2^32, col_begin + N at most 2^34.
  */
@@ -802,7 +804,8 @@ fm_status_t fm_layer_norm_bwd(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t bl
  * with scale NaN (a row of NaN, not of wrong numbers, in what is made of it).
  * Activations have a row for each token; a weight matrix [N, K] has a row, and so a
  * scale, for each output channel.
- *   dt  FM_F16, FM_BF16 or FM_F32: x [M, N];  q int8 [M, N];  scale fp32 [M].
+ *   dt  FM_F16, FM_BF16 or FM_F32: x [M, N];  q int8 [M, N], not overlapping x;  scale
+ *       fp32 [M].  M and N below 2^31.
  */
 fm_status_t fm_quant_i8(fm_dtype_t dt, int64_t M, int64_t N, const void* x, int8_t* q,
                         float* scale, hipStream_t stream);
@@ -816,8 +819,9 @@ fm_status_t fm_quant_i8(fm_dtype_t dt, int64_t M, int64_t N, const void* x, int8
  *   A        int8 [M, K] with a_scale fp32 [M];  W  int8 [N, K] (an output channel's
  *            weights in a row) with w_scale fp32 [N].  -128 may occur.
  *   bias     [N] or NULL: 0.   act  fm_act_t.   C  [M, N].
- *   K a multiple of 16, at most 131056 (the sums fit 32 bits); N a multiple of 8;
- *   w_scale 16-byte aligned.
+ *   K a multiple of 16, at most 131056 (the sums fit 32 bits); N a multiple of 8; M and
+ *   N below 2^22; w_scale 16-byte aligned.  C must not overlap the operands.  A NaN or
+ *   infinite scale stays in its row or column.
  */
 fm_status_t fm_gemm_i8(fm_dtype_t dt, fm_dtype_t c, int64_t M, int64_t N, int64_t K,
                        const int8_t* A, const float* a_scale, const int8_t* W,

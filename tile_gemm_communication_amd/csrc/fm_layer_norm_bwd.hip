@@ -5,8 +5,8 @@
 // of TH lanes at a time, the row lanes of all blocks taking rows in turn; at its end
 // the block writes one partial row a sum, and a second launch joins the partial
 // rows in order (no atomics: the same bits on every call).  Bound by the bytes of the
-// [M, N] arrays: 16384 x 4096 bf16 131 us, 5.1 TB/s, 5 of it the join; 4088 x 12288 fp32
-// 193 us, 4.7 TB/s, 10 of it the join.
+// [M, N] arrays: 16384 x 4096 bf16 130 us, 5.2 TB/s, 4 of it the join; 4088 x 12288 fp32
+// 192 us, 4.7 TB/s, 8 of it the join; 61 x 2816 8.8 us, two launches.
 #include <algorithm>
 
 #include "fm_layer_norm.hpp"
@@ -220,6 +220,32 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
   flush(acc_b, a.part_b);
 }
 
+struct LnJoinArgs {
+  const float* part[3];   // [rows, N] each
+  float* to[3];
+  int rows, N;
+};
+
+// Column sums of the partial rows, blockIdx.x which: 64 columns (16 lanes of four) and 16
+// slices of the rows a block, joined in order.
+__global__ __launch_bounds__(256) void layer_norm_join(const LnJoinArgs a) {
+  __shared__ f32x4 s[16][16];
+  const int col = (int)threadIdx.x % 16, slice = threadIdx.x / 16, e = blockIdx.y * 64 + col * 4;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  if (e < a.N) {
+    const float* p = a.part[blockIdx.x] + e;
+#pragma unroll 8
+    for (int r = slice; r < a.rows; r += 16) sum += *reinterpret_cast<const f32x4*>(p + (int64_t)r * a.N);
+  }
+  s[slice][col] = sum;
+  __syncthreads();
+  if (slice == 0 && e < a.N) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) sum += s[i][col];
+    *reinterpret_cast<f32x4*>(a.to[blockIdx.x] + e) = sum;
+  }
+}
+
 int64_t rows_of_block(int64_t N) {
   int64_t rows = 1;
 #define FM_LN_ROWS(TH, CH) rows = ln_rows<TH>()
@@ -301,28 +327,25 @@ extern "C" fm_status_t fm_layer_norm_bwd(fm_dtype_t dt, fm_dtype_t stream_dt, fm
     a.d = make_dropout(p, rng, draw, row_begin, 0);
   }
   float* part = static_cast<float*>(ws);
-  JoinArgs j = {};
+  LnJoinArgs j = {};
+  j.rows = (int)blocks;
+  j.N = (int)N;
   int n = 0;
   auto want = [&](float* to, float*& slot) {
     if (!to) return;
     slot = part;
     j.part[n] = part;
-    j.to[n] = to;
-    j.rows[n] = blocks;
-    j.first[n] = n;
-    ++n;
+    j.to[n++] = to;
     part += blocks * N;
   };
   want(d_bias, a.part_bias);
   want(d_w, a.part_w);
   want(d_b, a.part_b);
-  for (int i = n; i < 3; ++i) j.first[i] = 0x7fffffff;
-  j.N = N;
   if (M == 0 && n == 0) return FM_OK;
   if (M > 0) {
     if (dt == FM_F16) launch_types<F16>(stream_dt, block_dt, a, blocks, stream);
     else launch_types<BF16>(stream_dt, block_dt, a, blocks, stream);
   }
-  if (n > 0) launch_norm_join(j, n, stream);
+  if (n > 0) hipLaunchKernelGGL(layer_norm_join, dim3(n, (unsigned)cdiv(N, 64)), dim3(256), 0, stream, j);
   return launch_status();
 }

@@ -20,18 +20,6 @@ struct NormArgs {
 fm_status_t check_norm(fm_dtype_t dt, fm_dtype_t stream_dt, fm_dtype_t block_dt, int64_t M,
                        int64_t N, const void* gate, int64_t n_gates);
 
-// Column sums of partial rows (fm_norm_bwd.hip): up to three results, each of n
-// rows that are the sums of rows[i] partial rows; first[i] is the first result row
-// of result i among `total`, 0x7fffffff where there is none.
-struct JoinArgs {
-  const float* part[3];
-  float* to[3];
-  int64_t rows[3];   // partial rows of one result row
-  int64_t N;
-  int first[3];      // first blockIdx.x of each
-};
-void launch_norm_join(const JoinArgs& j, int total, hipStream_t stream);
-
 template <typename E>
 __device__ __forceinline__ typename Raw4<E>::type raw4(const void* p, int e) {
   return *reinterpret_cast<const typename Raw4<E>::type*>(

@@ -185,6 +185,14 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd(const NormBwdArgs a) {
   flush(acc_gate, a.part_gate);
 }
 
+struct JoinArgs {
+  const float* part[3];
+  float* to[3];
+  int64_t rows[3];   // partial rows of one result row
+  int64_t N;
+  int first[3];      // first blockIdx.x of each
+};
+
 // Column sums of the partial rows: a block takes 64 columns (16 lanes of four)
 // and 64 slices of the rows, joined in order.
 __global__ __launch_bounds__(1024) void norm_join(const JoinArgs a) {
@@ -266,11 +274,6 @@ void launch_types(fm_dtype_t stream_dt, fm_dtype_t block_dt, const NormBwdArgs& 
 }
 
 }  // namespace
-
-void launch_norm_join(const JoinArgs& j, int total, hipStream_t stream) {
-  hipLaunchKernelGGL(norm_join, dim3(total, cdiv(j.N, 64)), dim3(1024), 0, stream, j);
-}
-
 }  // namespace fm
 
 using namespace fm;
@@ -354,6 +357,7 @@ extern "C" fm_status_t fm_norm_residual_bwd(
     if (dt == FM_F16) launch_types<F16>(stream_dt, block_dt, a, sp.blocks, stream);
     else launch_types<BF16>(stream_dt, block_dt, a, sp.blocks, stream);
   }
-  if (n > 0) launch_norm_join(j, y, stream);
+  if (n > 0)
+    hipLaunchKernelGGL(norm_join, dim3(y, cdiv(N, 64)), dim3(1024), 0, stream, j);
   return launch_status();
 }
