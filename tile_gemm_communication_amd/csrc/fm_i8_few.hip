@@ -68,9 +68,9 @@ __device__ __forceinline__ void store_row4(const I8Args& a, const Finish4& f, i3
   else store4<BF16>(reinterpret_cast<__bf16*>(a.C) + at, v[0]);
 }
 
-// The rows of x as codes at `codes`, zeros from K to the
-// end of the last step, and their scales; the loads first, so that the weights' can
-// follow them before `start()` returns.  Ends behind a barrier.
+// The rows of x as codes at `codes`, zeros from K to the end of the last step, and their
+// scales.  x's loads come first, then start() (the weights' first loads), so that x does
+// not wait for the weights.  Ends behind a barrier.
 template <class F>
 __device__ __forceinline__ void quantise_rows(const I8Args& a, int w, int lane, int KT, char* codes,
                                               uint32_t* tops, float* scales, F&& start) {

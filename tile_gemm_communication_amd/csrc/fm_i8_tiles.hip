@@ -32,9 +32,9 @@ __device__ __forceinline__ void finish8(const I8Args& a, const Columns& c, const
   store8<O>(reinterpret_cast<typename Elem<O>::type*>(a.C) + at, v);
 }
 
-// A persistent grid of macro-tiles (fm_sched.hpp's order).  The epilogue turns each
-// 32-row block of a wave around through its own part of LDS, finished and rounded, so
-// that stores cover whole pieces of rows.
+// A persistent grid of macro-tiles (fm_sched.hpp's order).  The epilogue turns the sums of
+// each 32-row block of a wave around through its own part of LDS, so that a lane finishes
+// eight neighbouring columns of several rows and stores cover whole pieces of rows.
 template <typename E, typename O, int BM, int BN, int AHEAD>
 __global__ __launch_bounds__(256, 1) void gemm_i8_tiles(const TileArgs a) {
   using Tile = I8Tile<BM, BN, AHEAD>;
@@ -108,7 +108,8 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tiles(const TileArgs a) {
 // alone, of each of two there, and a tile's fixed part (us).  Fitted to 180 products of
 // 65..8192 rows, 1024..12288 columns and as much k (the choice is 0.5% slower than the best
 // of the seven on average; 64 x 64 tiles for all would be 26%, 256 x 256 for all 120%).  The
-// small tiles are bound by what a compute unit gets from L2 (16 KiB a step in 0.2 us), the
+// small tiles are bound by a compute unit's own load path (16 KiB a step in 0.2 us, 40 bytes a
+// cycle, with 32 tiles on the chip as with 192; deeper rings or more waves do not move it), the
 // large ones by the matrix cores under the power limit.
 struct TileChoice {
   int bm, bn, resident;
