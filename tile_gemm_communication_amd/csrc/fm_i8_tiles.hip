@@ -15,22 +15,10 @@ struct TileArgs : I8Args {
   int tiles_m, tiles_n, group_m;
 };
 
-// Eight results of a row: the sums' scales, bias, activation, rounding.
+// A lane's eight columns.
 struct Columns {
   f32x4 scale[2], bias[2];
 };
-
-template <typename O>
-__device__ __forceinline__ void finish8(const I8Args& a, const Columns& c, const i32x4 (&sum)[2], float sa,
-                                        int64_t at) {
-  f32x4 v[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[h][i] = (float)sum[h][i] * (sa * c.scale[h][i]) + c.bias[h][i];
-  activate_all(v, a.act);
-  store8<O>(reinterpret_cast<typename Elem<O>::type*>(a.C) + at, v);
-}
 
 // A persistent grid of macro-tiles (fm_sched.hpp's order).  The epilogue turns the sums of
 // each 32-row block of a wave around through its own part of LDS, so that a lane finishes
@@ -89,13 +77,30 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tiles(const TileArgs a) {
               i32x4{s[4 * r], s[4 * r + 1], s[4 * r + 2], s[4 * r + 3]};
         }
       wave_lds_sync();
-#pragma unroll 2
-      for (int q = 0; q < 32 * LPR / 64; ++q) {
-        const int y = q * (64 / LPR) + t.lane / LPR, m = t.wm * Tile::WM + 32 * i + y;
-        if (m < rows && mine) {
-          const i32x4* p = reinterpret_cast<const i32x4*>(stage + y * PITCH + x * 4);
-          const i32x4 sum[2] = {p[0], p[1]};
-          finish8<O>(a, c, sum, s_row[m], (m0 + m) * a.N + n0 + n);
+      // several rows' reads first, then their arithmetic: one wave a SIMD has no other to
+      // cover LDS's latency
+      constexpr int ROWS = 32 * LPR / 64, G = ROWS < 4 ? ROWS : 4;
+#pragma unroll 1
+      for (int q = 0; q < ROWS; q += G) {
+        f32x4 v[2 * G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int y = (q + g) * (64 / LPR) + t.lane / LPR;
+          const i32x4* p = reinterpret_cast<const i32x4*>(stage + y * PITCH + min(x, Tile::WN - 8) * 4);
+          const float sa = s_row[t.wm * Tile::WM + 32 * i + y];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[2 * g + h][k] = (float)p[h][k] * (sa * c.scale[h][k]) + c.bias[h][k];
+        }
+        activate_all(v, a.act);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int m = t.wm * Tile::WM + 32 * i + (q + g) * (64 / LPR) + t.lane / LPR;
+          if (m < rows && mine) {
+            const f32x4 o[2] = {v[2 * g], v[2 * g + 1]};
+            store8<O>(reinterpret_cast<typename Elem<O>::type*>(a.C) + (m0 + m) * a.N + n0 + n, o);
+          }
         }
       }
       wave_lds_sync();
