@@ -284,6 +284,26 @@ def test_what_is_dropped_has_no_part():
     assert all(torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(*got))
 
 
+@pytest.mark.parametrize("N", [128, 4096, 12288])
+def test_rows_far_from_zero(N):
+    """Mean 1000 and deviation 1: the variance is taken of the centred row, so it loses what
+    the mean's own rounding (32 u of 1000) costs, not 10^6 times that."""
+    import torch
+    rng = np.random.default_rng(N)
+    z = (1000 + rng.standard_normal((7, N))).astype(np.float32)
+    w = _dev(np.ones(N), "bf16")
+    mean, rstd = torch.empty(7, device="cuda:0"), torch.empty(7, device="cuda:0")
+    y16 = torch.empty(7, N, dtype=torch.float16, device="cuda:0")
+    fm.fm_layer_norm(None, y16, resid=_dev(z, "fp32"), w=w.half(), mean=mean, rstd=rstd)
+    ref, m = z.astype(np.float64), z.astype(np.float64).mean(1)
+    r = 1 / np.sqrt(ref.var(1) + EPS)
+    off = 32 * U * 1005                      # of the mean
+    assert (np.abs(_host(mean) - m) <= off).all()
+    assert (np.abs(_host(rstd) / r - 1) <= off * off + 40 * U).all()
+    yr = (ref - m[:, None]) * r[:, None]
+    assert (np.abs(_host(y16) - yr) <= off * r[:, None] + 64 * U * np.abs(yr) + HALF["fp16"] * np.abs(yr) + 1e-7).all()
+
+
 def test_rows_with_nan_are_their_own():
     import torch
     x = torch.randn(5, 512, device="cuda:0")
