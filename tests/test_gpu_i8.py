@@ -143,6 +143,77 @@ def test_gemm(M, N, K):
         assert (err <= _limit(ref, v, mag, act, to)).all(), (dt, to, err.max())
 
 
+# Sizes whose rounds choose each macro-tile, with one to nine K steps, whole and ragged
+# ones, and edges in both directions.
+TILED = {
+    "64x64": [(301, 520, 128), (301, 520, 16), (301, 520, 256), (301, 520, 144), (301, 520, 384), (301, 520, 272),
+              (301, 520, 400), (301, 520, 1040)],
+    "64x128": [(3599, 520, 128), (3599, 520, 16), (3599, 520, 144), (3599, 520, 272), (3599, 520, 400), (1853, 520, 1040)],
+    "128x128": [(3599, 520, 1024), (3599, 520, 1040)],
+    "128x192": [(2920, 2056, 384), (2920, 2056, 272), (2920, 2056, 400), (7285, 520, 656), (7285, 520, 1024), (7285, 520, 1040)],
+    "256x128": [(5442, 1032, 384), (5442, 1032, 272), (5442, 1032, 400), (398, 12296, 656), (398, 12296, 1024), (398, 12296, 1040)],
+    "256x192": [(5830, 2056, 128), (5830, 2056, 16), (5830, 2056, 256), (5830, 2056, 144), (4860, 2056, 384), (4860, 2056, 272),
+                (4860, 2056, 400), (7285, 1032, 656), (7285, 1032, 1024), (7285, 1032, 1040)],
+    "256x256": [(6800, 2056, 128), (6800, 2056, 16), (980, 12296, 256), (980, 12296, 144), (980, 12296, 384), (980, 12296, 272),
+                (883, 12296, 400), (883, 12296, 656), (786, 12296, 1024), (786, 12296, 1040)],
+}
+
+
+@pytest.mark.parametrize("M,N,K,tile", [(*s, t) for t, ss in TILED.items() for s in ss])
+def test_gemm_of_every_tile(M, N, K, tile):
+    """Against float64 sums on the GPU (exact: below 2^53), by plain matrix products."""
+    import torch
+    say(f"gemm i8 tile {tile}: M={M} N={N} K={K}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + N + K)
+    A = torch.randint(-128, 128, (M, K), generator=g, device="cuda").to(torch.int8)
+    W = torch.randint(-128, 128, (N, K), generator=g, device="cuda").to(torch.int8)
+    sa = 0.5 + torch.rand(M, generator=g, device="cuda")
+    sw = (0.5 + torch.rand(N, generator=g, device="cuda")) / (5461 * K ** 0.5)
+    sums = A.double() @ W.double().t().contiguous()
+    for dt, to, act in ((torch.bfloat16, torch.bfloat16, 2), (torch.float16, torch.float32, 0)):
+        b = torch.randn(N, generator=g, device="cuda").to(dt) if act else None
+        C, end = _sentinels((M, N), to)
+        fm.fm_gemm_i8(A, sa, W, sw, C, bias=b, act=act)
+        v = sums * (sa.double()[:, None] * sw.double())
+        mag = v.abs()
+        if act:
+            v, mag = v + b.double(), mag + b.double().abs()
+            u = 0.7978845608028654 * (v + 0.044715 * v ** 3)
+            ref, z = 0.5 * v * (1 + torch.tanh(u)), 1.6 * (v.abs() + 0.0447 * v.abs() ** 3)
+        else:
+            ref, z = v, 0 * v
+        name = {torch.bfloat16: "bf16", torch.float32: "fp32"}[to]
+        lim = 1.13 * 4 * U * mag + (10 * z + 8) * U * ref.abs() + HALF[name] * ref.abs() + TINY[name]
+        assert (end == -7).all()
+        assert ((C.double() - ref).abs() <= lim).all(), (to, act)
+
+
+@pytest.mark.parametrize("N", [2040, 2056, 4104, 6152, 8192, 12296])
+@pytest.mark.parametrize("M", [1, 7, 8, 9, 16, 17, 32, 33, 48, 49, 64])
+def test_few_rows(M, N):
+    """Every number of rows at an edge, with one to six eights of columns a block, over k of less
+    than a step, whole steps, tails, and more steps than a wave's ring holds: the product
+    against float64 sums on the GPU, and the layer on 16-bit rows against the product."""
+    import torch
+    say(f"few rows M={M} N={N}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + N)
+    for K in (16, 128, 1040, 1536, 4112, 6144):
+        x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+        q, s = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+        fm.fm_quant_i8(x, q, s)
+        W = torch.randint(-128, 128, (N, K), generator=g, device="cuda").to(torch.int8)
+        sw = (0.5 + torch.rand(N, generator=g, device="cuda")) / (70 * K ** 0.5)
+        C, end = _sentinels((M, N), torch.float32)
+        fm.fm_gemm_i8(q, s, W, sw, C)
+        ref = (q.double() @ W.double().t().contiguous()) * (s.double()[:, None] * sw.double())
+        assert (end == -7).all() and ((C.double() - ref).abs() <= 4 * U * ref.abs() + 1e-38).all(), K
+        L, end = _sentinels((M, N), torch.float32)
+        fm.fm_linear_i8(x, W, sw, L, ws=fm.linear_i8_workspace(M, K))
+        assert (end == -7).all() and torch.equal(L, C), K
+
+
 def test_gemm_of_the_largest_sums():
     """Every product 2^14: the sum of 131056 of them is 2^31 less 2^18."""
     import torch
