@@ -5,8 +5,8 @@
 // keeps a ring of S steps in its own part of LDS, filled by direct-to-LDS loads of eight
 // whole 128-byte pieces of rows, so that S - 1 steps are in flight without a register or
 // a barrier; the waves' sums (whole numbers: exact in any order) meet in LDS at the end.
-// Bound by the weights' bytes: 1 x 6144 x 12288 (k x columns) 12.4 us, 6.1 TB/s, with the
-// weights in the Infinity Cache, 15.1 from HBM; 45 x 12288 x 6144 14.6 and 22.2, where a wave's
+// Bound by the weights' bytes: 1 x 6144 x 12288 (k x columns) 12.3 us, 6.1 TB/s, with the
+// weights in the Infinity Cache, 14.8 from HBM; 45 x 12288 x 6144 14.5 and 21.8, where a wave's
 // loads of x and W return in one order (macro-tiles took 24.8 and the k loop's latency).
 //
 // v_mfma_i32_16x16x64_i8: lane l holds 16 bytes of row l % 16 from k = 16 (l / 16) on of
@@ -16,6 +16,7 @@
 
 #include "fm_i8.hpp"
 #include "fm_i8_tile.hpp"
+#include "fm_sched.hpp"
 
 namespace fm {
 namespace {
@@ -125,7 +126,9 @@ __global__ __launch_bounds__((64 * FewShape<X8, C8, QUANT>::NWV)) void gemm_i8_f
   __shared__ float s_scale[kFewQuantRows];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int M = (int)a.M, K = (int)a.K;
-  const int64_t n0 = (int64_t)blockIdx.x * (8 * C8);
+  // an XCD takes neighbouring columns: 64 x 8192 x 8192 14.3 us, dealt out in turn 21.0 (rows of
+  // W whose pitch is a power of two); 32 x 4096 x 4096 5.5 and 6.7; 24 x 6144 x 6144 8.7 and 8.5
+  const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(xcd_slot(blockIdx.x, gridDim.x)) * (8 * C8);
   const int cols = (int)min((int64_t)(8 * C8), a.N - n0);
   const int KT = (K + kI8Step - 1) / kI8Step, tail = K % kI8Step;
   const char* const wt = a.W + n0 * K;

@@ -113,9 +113,10 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tiles(const TileArgs a) {
 // alone, of each of two there, and a tile's fixed part (us).  Fitted to 180 products of
 // 65..8192 rows, 1024..12288 columns and as much k (the choice is 0.5% slower than the best
 // of the seven on average; 64 x 64 tiles for all would be 26%, 256 x 256 for all 120%).  The
-// small tiles are bound by a compute unit's own load path (16 KiB a step in 0.2 us, 40 bytes a
-// cycle, with 32 tiles on the chip as with 192; deeper rings or more waves do not move it), the
-// large ones by the matrix cores under the power limit.
+// small tiles take 0.2 us for the 16 KiB of a step with 32 tiles on the chip as with 192, with
+// twice the stages or with a ring for each wave instead (loads alone reach 145 GB/s a unit, so
+// it is not their path by itself); the large ones are bound by the matrix cores under the power
+// limit.
 struct TileChoice {
   int bm, bn, resident;
   double alone, shared, fixed;
