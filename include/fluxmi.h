@@ -102,11 +102,11 @@ typedef enum fm_dtype {
     FM_F32 = 2
 } fm_dtype_t;
 
-/* Activation applied to MoE layer 0's fp32 result before it is rounded and
- * stored (fm_moe_gather_gemm_act). */
+/* Activation applied to the fp32 result of MoE layer 0 (fm_moe_gather_gemm_act) or of
+ * an 8-bit product (fm_gemm_i8) before it is rounded and stored. */
 typedef enum fm_act {
     FM_ACT_NONE = 0,       /* H = X W1, as fm_moe_gather_gemm */
-    FM_ACT_RELU = 1,       /* max(x, 0) */
+    FM_ACT_RELU = 1,       /* max(x, 0); of a NaN 0 in the MoE products, NaN in the 8-bit ones */
     FM_ACT_GELU_TANH = 2,  /* x/2 * (1 + tanh(sqrt(2/pi) * (x + 0.044715 x^3))) */
     FM_ACT_SILU = 3        /* x / (1 + exp(-x)) */
 } fm_act_t;
@@ -821,7 +821,7 @@ fm_status_t fm_quant_i8(fm_dtype_t dt, int64_t M, int64_t N, const void* x, int8
  *   bias     [N] or NULL: 0.   act  fm_act_t.   C  [M, N].
  *   K a multiple of 16, at most 131056 (the sums fit 32 bits); N a multiple of 8; M and
  *   N below 2^22; w_scale 16-byte aligned.  C must not overlap the operands.  A NaN or
- *   infinite scale stays in its row or column.
+ *   infinite scale stays in its row or column, a NaN under every activation.
  */
 fm_status_t fm_gemm_i8(fm_dtype_t dt, fm_dtype_t c, int64_t M, int64_t N, int64_t K,
                        const int8_t* A, const float* a_scale, const int8_t* W,

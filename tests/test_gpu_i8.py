@@ -301,3 +301,28 @@ def test_extremes_of_scales():
         fm.fm_gemm_i8(A, sa, W, sw, C)
         ref = 64.0 * sa[:, None] * sw
         assert torch.equal(C.nan_to_num(7, 8), ref.nan_to_num(7, 8))
+
+
+@pytest.mark.parametrize("act", [0, 1, 2, 3])
+@pytest.mark.parametrize("M,K", [(4, 512), (4, 16384), (40, 512), (70, 512), (300, 512)])
+def test_nan_under_every_activation(M, K, act):
+    """A row with a NaN, or too large for its scale, and a row or column with a NaN scale stay NaN
+    whatever the activation: rows quantised in the product's blocks, before it, and on tiles."""
+    import torch
+    N = 72
+    x = torch.randn(M, K, device="cuda:0").bfloat16()
+    x[1, K - 1], x[2, 3] = float("nan"), 2.0 ** 120
+    W = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda:0")
+    sw, bias = 0.01 * torch.rand(N, device="cuda:0") + 1e-3, torch.randn(N, device="cuda:0").bfloat16()
+    sw[5] = float("nan")
+    bad = torch.zeros(M, N, dtype=torch.bool, device="cuda:0")
+    bad[1:3], bad[:, 5] = True, True
+    C = torch.empty(M, N, device="cuda:0")
+    fm.fm_linear_i8(x, W, sw, C, bias=bias, act=act, ws=fm.linear_i8_workspace(M, K))
+    assert torch.equal(C.isnan(), bad) and not C.isinf().any()
+    q, s = torch.empty(M, K, dtype=torch.int8, device="cuda:0"), torch.empty(M, device="cuda:0")
+    fm.fm_quant_i8(x, q, s)
+    for to in (torch.float32, torch.bfloat16):
+        C = torch.empty(M, N, dtype=to, device="cuda:0")
+        fm.fm_gemm_i8(q, s, W, sw, C, bias=bias, act=act)
+        assert torch.equal(C.isnan(), bad) and not C.isinf().any()
