@@ -21,14 +21,13 @@
 // column 8 r + 4 (l / 32) + q: runs of four columns.
 #pragma once
 
+#include "fm_i8_choice.hpp"
 #include "fm_tile.hpp"
 
 namespace fm {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-
-constexpr int kI8Step = 128;   // bytes of k in a stage
 
 template <int BM, int BN, int AHEAD>
 struct I8Tile {
