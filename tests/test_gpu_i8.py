@@ -326,3 +326,22 @@ def test_nan_under_every_activation(M, K, act):
         C = torch.empty(M, N, dtype=to, device="cuda:0")
         fm.fm_gemm_i8(q, s, W, sw, C, bias=bias, act=act)
         assert torch.equal(C.isnan(), bad) and not C.isinf().any()
+
+
+# Sizes with more tiles than blocks (two a unit of the two small ones) and an uneven last round,
+# over whole and ragged steps of k.
+ROUNDS = {
+    "64x64": [(6529, 520, 384), (6529, 520, 1040), (6529, 520, 144)],
+    "64x128": [(7233, 520, 384), (7233, 520, 400), (7169, 1032, 1024), (513, 12296, 656)],
+    "128x128": [(513, 12296, 1024), (513, 12296, 1040)],
+    "128x192": [(14529, 1032, 1024), (14529, 1032, 656)],
+    "256x128": [(13057, 1032, 384), (13057, 1032, 272)],
+    "256x192": [(1409, 12296, 1024), (11521, 2056, 400)],
+    "256x256": [(1793, 12296, 1024), (1857, 12296, 400), (11777, 2056, 272), (7425, 4104, 128)],
+}
+
+
+@pytest.mark.parametrize("M,N,K,tile", [(*s, t) for t, ss in ROUNDS.items() for s in ss])
+def test_blocks_that_take_several_tiles(M, N, K, tile):
+    """The next tile's loads land where the last one's results were staged; every element."""
+    test_gemm_of_every_tile(M, N, K, tile)

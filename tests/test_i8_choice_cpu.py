@@ -7,7 +7,7 @@ import subprocess
 
 import pytest
 
-from test_gpu_i8 import TILED
+from test_gpu_i8 import ROUNDS, TILED
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "tile_gemm_communication_amd", "csrc")
@@ -48,3 +48,11 @@ def choose(tmp_path_factory):
 @pytest.mark.parametrize("tile", TILED)
 def test_sizes_take_the_tile_they_are_named_for(choose, tile):
     assert [t for t, _ in choose(TILED[tile])] == [tile] * len(TILED[tile])
+
+
+@pytest.mark.parametrize("tile", ROUNDS)
+def test_sizes_take_several_tiles_a_block(choose, tile):
+    bm, bn = map(int, tile.split("x"))
+    for (M, N, K), (got, resident) in zip(ROUNDS[tile], choose(ROUNDS[tile])):
+        tiles = -(-M // bm) * -(-N // bn)
+        assert got == tile and tiles > UNITS * resident and tiles % (UNITS * resident), (M, N, K, got)
