@@ -345,3 +345,29 @@ ROUNDS = {
 def test_blocks_that_take_several_tiles(M, N, K, tile):
     """The next tile's loads land where the last one's results were staged; every element."""
     test_gemm_of_every_tile(M, N, K, tile)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,K", [(1, 16384), (1, 16368), (1, 15888), (2, 8192), (3, 5120), (4, 4096), (5, 3056), (6, 2560),
+                                 (7, 2048), (8, 2048), (8, 2032), (8, 1552), (8, 16)])
+def test_most_that_a_block_quantises(M, K, dt):
+    """Up to 32 pieces of 512 values, the last one ragged too: codes and scales of the
+    definition (exact for 16-bit rows), so the same bits as of the two calls, and the float64 product."""
+    import torch
+    N = 520
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + K)
+    x = (torch.randn(M, K, generator=g, device="cuda") * (1 + torch.arange(M, device="cuda")[:, None])).to(_dtype(dt))
+    x[M - 1, K - 1] = 40.0                   # a row's largest in its last piece
+    W = torch.randint(-128, 128, (N, K), generator=g, device="cuda").to(torch.int8)
+    sw = (0.5 + torch.rand(N, generator=g, device="cuda")) / (70 * K ** 0.5)
+    L, end = _sentinels((M, N), torch.float32)
+    fm.fm_linear_i8(x, W, sw, L, ws=fm.linear_i8_workspace(M, K))
+    assert (end == -7).all()
+    rq, rs = od.quant(_host(x))
+    ref = od.gemm_i8(rq, rs, W.cpu().numpy(), _host(sw), None, 0)[0]
+    assert (np.abs(_host(L) - ref) <= 5 * U * np.abs(ref) + 1e-38).all()
+    q, s, C = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda"), torch.empty_like(L)
+    fm.fm_quant_i8(x, q, s)
+    fm.fm_gemm_i8(q, s, W, sw, C)
+    assert torch.equal(L, C)
