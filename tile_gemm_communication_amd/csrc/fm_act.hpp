@@ -36,7 +36,8 @@ __device__ __forceinline__ void activate_all(f32x4 (&v)[N], int act) {
   };
   constexpr float kLog2e = 1.4426950408889634f, kGelu = -2.f * 0.7978845608028654f * kLog2e;
   switch (act) {
-    case FM_ACT_RELU: return each([](float x) { return x < 0.f ? 0.f : x; });   // a NaN stays one
+    case FM_ACT_RELU:   // a NaN stays one, in one instruction
+      return each([](float x) { return __builtin_elementwise_maximum(x, 0.f); });
     case FM_ACT_GELU_TANH:
       return each([&](float x) { return gated(x, x * fmaf(kGelu * 0.044715f, x * x, kGelu)); });
     case FM_ACT_SILU: return each([&](float x) { return gated(x, x * -kLog2e); });
