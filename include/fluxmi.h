@@ -814,7 +814,8 @@ fm_status_t fm_quant_i8(fm_dtype_t dt, int64_t M, int64_t N, const void* x, int8
  * fm_gemm_i8 -- product of 8-bit rows:
  *   C[m, n] = act(a_scale[m] * w_scale[n] * sum_k A[m, k] * W[n, k] + bias[n]).
  * The sum is exact (32-bit integers); scales, bias and activation are applied in fp32
- * and the result is rounded once.
+ * and the result is rounded once.  a_scale[m] * w_scale[n] is taken first: past 2^128 a value
+ * is infinite, or NaN where the sum is 0; below 2^-126 it has fewer bits.
  *   dt       FM_F16 or FM_BF16: bias;  c  dt or FM_F32: C.
  *   A        int8 [M, K] with a_scale fp32 [M];  W  int8 [N, K] (an output channel's
  *            weights in a row) with w_scale fp32 [N].  -128 may occur.

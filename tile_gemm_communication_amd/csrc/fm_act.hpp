@@ -21,7 +21,8 @@ __device__ __forceinline__ float activate(float x, int act) {
 // The activations of N values, one branch for all: x / (1 + exp(-z)) as x times the
 // hardware's reciprocal (1 ulp) of 1 + 2^(-z log2 e), z's factors folded into two
 // constants.  A large tile's results are all finished at once with the matrix cores idle,
-// so its instructions count: GELU of 256 x 256 takes 7 of these against 22 with a division.
+// so its instructions count: GELU takes 7 vector instructions a value, 19 with a division
+// (4096 x 12288 x 6144 with its rows quantised: 283 us, so 305).
 // Where z overflows the limits hold: x or -0.
 template <int N>
 __device__ __forceinline__ void activate_all(f32x4 (&v)[N], int act) {

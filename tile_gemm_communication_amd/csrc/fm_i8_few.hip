@@ -24,8 +24,10 @@ namespace {
 constexpr int kFewLds = 152 * 1024;
 
 // What a block quantises for itself: at most 32 pieces of 512 values (four a wave; 17 KiB
-// of codes), in the shadow of the first weights' loads.  1 x 12288 x 6144: 14.7 us, with a
-// launch of its own before it 17.6; of 96 pieces (8 x 6144) it would take 23, against 15.9.
+// of codes).  A wave's pieces come one after another (each load has its own branch, and is
+// waited for at its end), and the first weights' loads go out behind the last.  1 x 12288 x
+// 6144: 14.7 us, the product alone 12.3, with a launch of its own before it 17.6; of 96 pieces
+// (8 x 6144) it would take 23, against 15.9.
 constexpr int kQuantPiece = 512, kQuantHeld = 4, kQuantMost = 8 * kQuantHeld;
 constexpr int kFewQuantRows = 8, kFewCodes = 17 * 1024;
 
@@ -70,8 +72,8 @@ __device__ __forceinline__ void store_row4(const I8Args& a, const Finish4& f, i3
 }
 
 // The rows of x as codes at `codes`, zeros from K to the end of the last step, and their
-// scales.  x's loads come first, then start() (the weights' first loads), so that x does
-// not wait for the weights.  Ends behind a barrier.
+// scales.  x's loads come first, then start() (the weights' first loads, in flight during
+// the arithmetic), so that x does not wait for the weights.  Ends behind a barrier.
 template <class F>
 __device__ __forceinline__ void quantise_rows(const I8Args& a, int w, int lane, int KT, char* codes,
                                               uint32_t* tops, float* scales, F&& start) {
@@ -126,8 +128,9 @@ __global__ __launch_bounds__((64 * FewShape<X8, C8, QUANT>::NWV)) void gemm_i8_f
   __shared__ float s_scale[kFewQuantRows];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int M = (int)a.M, K = (int)a.K;
-  // an XCD takes neighbouring columns: 64 x 8192 x 8192 14.3 us, dealt out in turn 21.0 (rows of
-  // W whose pitch is a power of two); 32 x 4096 x 4096 5.5 and 6.7; 24 x 6144 x 6144 8.7 and 8.5
+  // where the blocks are a multiple of 8, an XCD takes neighbouring columns: 64 x 8192 x 8192
+  // 14.3 us, dealt out in turn 21.0 (rows of W whose pitch is a power of two); 32 x 4096 x 4096
+  // 5.5 and 6.7; 24 x 6144 x 6144 8.7 and 8.5; other numbers of blocks are dealt out in turn
   const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(xcd_slot(blockIdx.x, gridDim.x)) * (8 * C8);
   const int cols = (int)min((int64_t)(8 * C8), a.N - n0);
   const int KT = (K + kI8Step - 1) / kI8Step, tail = K % kI8Step;
@@ -228,6 +231,9 @@ __global__ __launch_bounds__((64 * FewShape<X8, C8, QUANT>::NWV)) void gemm_i8_f
   }
 }
 
+// One block a unit up to 12288 columns on 256 units; a block takes most of a unit's LDS, so
+// more columns take a second, partly filled round: 1 x 6144 x 12288 (k x columns) 12.3 us,
+// 14336 17.1, 16384 21.0, 28672 35.5.
 template <int X8, bool QUANT>
 void launch_columns(const I8Args& a, hipStream_t stream) {
   const int64_t eights = a.N / 8, per = cdiv(eights, device_cu_count());

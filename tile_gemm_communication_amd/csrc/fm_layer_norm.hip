@@ -5,7 +5,9 @@
 // block and residual are read once and out and y written once: the operator is
 // bound by those bytes.  Mean, centred mean square and, for y in 8 bits, the largest
 // magnitude are the only exchanges between lanes.  16384 x 4096 bf16 with an fp32 block
-// 120 us, 5.6 TB/s (116 without dropout); 4088 x 12288 fp32 133 us; 1 x 4096 4 us, the call.
+// 120 us, 5.6 TB/s (116 without dropout; to 8 bits 113); 4088 x 12288 fp32 133 us; 1 x 4096
+// 4 us, the call.  A lane's loads follow one another, each operand's under its own branch: many
+// rows cover that, some hundred do not (509 x 4096 5.2 us, 3.2 TB/s).
 #include "fm_layer_norm.hpp"
 
 namespace fm {

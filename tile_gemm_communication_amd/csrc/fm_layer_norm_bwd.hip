@@ -42,7 +42,8 @@ __global__ __launch_bounds__(TH == 768 ? 768 : 1024) void layer_norm_bwd(const L
   constexpr f32x4 kZero = {0.f, 0.f, 0.f, 0.f};
   __shared__ f32x2 s_red[2][RW][(TH + 63) / 64];
   // Rows from 8200 elements on keep their sums in LDS, each lane's in places of its own; the
-  // registers hold the next row instead, which is on its way while this one is worked on.
+  // registers hold the next row instead, which is on its way while this one is worked on
+  // (the wait for it, at the row's end, is also one for this row's stores).
   // 1024 lanes have 128 registers each: the longest rows (from 12296 on) do without that,
   // and read d_out behind the barrier; of their sums LDS holds two.
   constexpr bool kRoom = CH == 1, kAhead = TH * CH < 2048, kBiasRoom = kRoom || !kAhead;
